@@ -25,6 +25,9 @@
 #include "bwd_f32.cuh"
 #include "proj_gemm.cuh"
 #include "win_bwd_tc.cuh"
+#include "rope.cuh"
+#include "short_conv.cuh"
+#include "ssm_scan.cuh"
 
 namespace {
 
@@ -2034,3 +2037,7 @@ extern "C" kta_status kta_gla_chunk_fwd_noalloc(const void* q, const void* k, co
   if (chunk == 32) return launch_gla_chunk_noalloc<64, 32>(L, st);
   return launch_gla_chunk_noalloc<64, 16>(L, st);
 }
+
+// =========================================================================== token mixers
+
+#include "mixer_api.cuh"

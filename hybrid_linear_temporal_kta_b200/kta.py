@@ -46,6 +46,32 @@ class HybridCfg(ctypes.Structure):
                 ("scale_softmax", ctypes.c_float), ("scale_gla", ctypes.c_float)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int), ("dims", ctypes.c_int * 4), ("begin", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("mscale", ctypes.c_float), ("pos", ctypes.c_void_p),
+                ("pos_per_seq", ctypes.c_int), ("pos0", ctypes.c_int64), ("freqs", ctypes.c_void_p)]
+
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_PARTS = 0, 1, 2, 3
+_ROPE_SCALING = {None: ROPE_PLAIN, "linear": ROPE_LINEAR, "base": ROPE_BASE, "by_parts": ROPE_BY_PARTS}
+
+
+class ShortConv(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "D", "K", "dtype", "silu")] + \
+               [(n, ctypes.c_void_p) for n in ("x", "w", "bias", "S0", "lens")]
+
+
+class Ssm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "D", "N", "G", "dtype")] + \
+               [(n, ctypes.c_void_p) for n in ("u", "dt", "A", "Bm", "Cm", "D_skip", "z", "dt_bias",
+                                               "S0", "lens")]
+
+
+class SsmGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dout", "dS_out", "du", "ddt", "dA", "dB", "dC",
+                                               "dD_skip", "dz", "ddt_bias", "dS0")]
+
+
 _vp, _i, _f, _st = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int
 _fp = ctypes.c_void_p
 
@@ -86,6 +112,18 @@ _SIGS = {
     "kta_stream_save": ([_vp, _vp, _vp], _st),
     "kta_stream_load": ([_vp, _vp, _vp], _st),
     "kta_stream_destroy": ([_vp], _st),
+    "kta_rope_freqs": ([_i] + [ctypes.c_double] + [_i] + [ctypes.c_double] * 4 + [_vp, _vp], _st),
+    "kta_rope_fwd": ([ctypes.POINTER(Rope), _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
+    "kta_rope_bwd": ([ctypes.POINTER(Rope), _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
+    "kta_short_conv_fwd": ([ctypes.POINTER(ShortConv), _vp, _vp, _vp], _st),
+    "kta_short_conv_bwd_workspace": ([ctypes.POINTER(ShortConv)], ctypes.c_size_t),
+    "kta_short_conv_bwd": ([ctypes.POINTER(ShortConv)] + [_vp] * 7 + [ctypes.c_size_t, _vp], _st),
+    "kta_ssm_scan_fwd_workspace": ([ctypes.POINTER(Ssm)], ctypes.c_size_t),
+    "kta_ssm_scan_fwd": ([ctypes.POINTER(Ssm), _vp, _fp, _vp, ctypes.c_size_t, _vp], _st),
+    "kta_ssm_scan_step": ([ctypes.POINTER(Ssm), _vp, _fp, _vp], _st),
+    "kta_ssm_scan_bwd_workspace": ([ctypes.POINTER(Ssm)], ctypes.c_size_t),
+    "kta_ssm_scan_bwd": ([ctypes.POINTER(Ssm), ctypes.POINTER(SsmGrads), _vp, ctypes.c_size_t, _vp],
+                         _st),
     "kta_device_status": ([_vp], _st),
     "kta_selftest_wait_timeout": ([ctypes.c_longlong, _vp], _st),
     "kta_trace_begin": ([], _st),
@@ -531,6 +569,322 @@ class Stream:
             self.close()
         except Exception:
             pass
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _want(t, name, dtype, shape, like):
+    """t must be a contiguous CUDA tensor of this dtype and shape on like's device."""
+    _need(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _io(t, name):
+    """dtype code of an operator's main tensor."""
+    _need(t, name)
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return _DT[t.dtype]
+
+
+class _on:
+    """The device and stream of one call: the tensors' device, and its current stream or the one
+    given. Memory allocated inside belongs to that stream (scratch may be reused as soon as the
+    call's work on it is done), and tensors of other streams that the call reads are recorded on it."""
+
+    def __init__(self, t, stream, reads=()):
+        self.dev, self.given, self.reads, self.old = t.device, stream, reads, None
+
+    def __enter__(self):
+        if self.given is None:
+            self.ctx = None if torch.cuda.current_device() == self.dev.index else \
+                torch.cuda.device(self.dev)
+            if self.ctx is not None:
+                self.ctx.__enter__()
+            return _vp(torch.cuda.current_stream(self.dev).cuda_stream)
+        if self.given.device != self.dev:
+            raise ValueError(f"stream belongs to {self.given.device}, the tensors to {self.dev}")
+        if not torch.cuda.is_current_stream_capturing():
+            for t in self.reads:
+                if t is not None:
+                    t.record_stream(self.given)
+        self.ctx = torch.cuda.stream(self.given)
+        self.ctx.__enter__()
+        return _vp(self.given.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _scratch(n, like):
+    return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+
+
+def rope_freqs(dims, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(freqs, mscale) of rope_fwd: radians per position of every pair, fp64 on `device`, for one
+    section of `dims` dims or a tuple of them (one per axis). scaling: None, "linear", "base" (the
+    base raised so that only long wavelengths stretch) or "by_parts" (needs orig_len), for contexts
+    `factor` times longer."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {tuple(_ROPE_SCALING)}")
+    out, m = [], ctypes.c_float(1.0)
+    for r in (dims,) if isinstance(dims, int) else tuple(dims):
+        f = (ctypes.c_double * max(1, r // 2))()
+        _check(_lib.kta_rope_freqs(r, base, _ROPE_SCALING[scaling], factor, orig_len, beta_fast,
+                                   beta_slow, ctypes.cast(f, _vp), ctypes.byref(m)), "kta_rope_freqs")
+        out += list(f)
+    return torch.tensor(out, dtype=torch.float64, device=device), float(m.value)
+
+
+def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, stream):
+    dt = _io(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, H, d]")
+    B, N, Hq, d = q.shape
+    dims = (dims,) if isinstance(dims, int) else tuple(dims)
+    if not 1 <= len(dims) <= 4:
+        raise ValueError("1 to 4 axes")
+    if layout not in ("half", "interleaved"):
+        raise ValueError('layout must be "half" or "interleaved"')
+    _want(freqs, "freqs", torch.float64, (sum(dims) // 2,), q)
+    per_seq = 0
+    if pos is not None:
+        _need(pos, "pos", torch.int64)
+        if pos.device != q.device:
+            raise ValueError(f"pos is on {pos.device}, expected {q.device}")
+        A, shape = len(dims), tuple(pos.shape)
+        if shape == (B, N, A) or (A == 1 and shape == (B, N)):
+            per_seq = 1
+        elif not (shape == (N, A) or (A == 1 and shape == (N,))):
+            raise ValueError(f"pos must be [N, axes] or [B, N, axes] (one axis: [N] or [B, N]), got "
+                             f"{shape}")
+    if k is not None:
+        _need(k, "k", q.dtype)
+        if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+            raise ValueError("k must have q's batch, tokens and head dim")
+        if k.device != q.device:
+            raise ValueError(f"k is on {k.device}, expected {q.device}")
+    xs = (q,) if k is None else (q, k)
+    ranges = []
+    for x in xs:
+        h0, h1 = (0, x.shape[2]) if heads is None else heads
+        if not 0 <= h0 < h1 <= x.shape[2]:
+            raise ValueError(f"heads {heads} outside 0..{x.shape[2]}")
+        ranges.append((h0, h1))
+    if out is not None:
+        out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(out) != len(xs):
+            raise ValueError("out must have one tensor for each input")
+        for o, x in zip(out, xs):
+            _want(o, "out", x.dtype, x.shape, x)
+    cfg = Rope(len(dims), (ctypes.c_int * 4)(*dims), begin, int(layout == "interleaved"), mscale,
+               _at(pos), per_seq, pos0, _at(freqs))
+    with _on(q, stream, (q, k, freqs, pos) + (out or ())) as st:
+        o = out if out is not None else tuple(torch.empty_like(x) for x in xs)
+        ptr = [v for x, y, (h0, _) in zip(xs, o, ranges) for v in (_ptr(x, h0 * d), _ptr(y, h0 * d))]
+        ptr += [None] * (4 - len(ptr))
+        hs = [v for x, (h0, h1) in zip(xs, ranges) for v in (h1 - h0, x.shape[2])]
+        hs += [0] * (4 - len(hs))
+        _check(fn(ctypes.byref(cfg), *ptr, Shape(B, 1, N, d, dt), *hs, st), fn.__name__)
+    return o[0] if k is None else o
+
+
+def rope_fwd(q, k=None, *, freqs, dims, begin: int = 0, layout: str = "half", mscale: float = 1.0,
+             pos=None, pos0: int = 0, heads=None, out=None, stream=None):
+    """Rotary positions of q (and of k, in the same launch) [B, N, H, d], bf16 or fp32: dims
+    [begin, begin + sum(dims)) of each head, one section of `dims` per position axis, turn by
+    pos * freqs (rope_freqs); the others are copied. pos: int64 [N, axes] or [B, N, axes] (one axis:
+    [N], [B, N] or None = the token's place); pos0 is added to axis 0. Only the heads in range are
+    written (fresh buffers are uninitialised elsewhere); out = the inputs rotates in place. Returns o
+    or (o_q, o_k)."""
+    return _rope(_lib.kta_rope_fwd, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out,
+                 stream)
+
+
+def rope_bwd(dq, dk=None, *, freqs, dims, begin: int = 0, layout: str = "half", mscale: float = 1.0,
+             pos=None, pos0: int = 0, heads=None, out=None, stream=None):
+    """Gradient of rope_fwd: the rotation of dq (and dk) by the opposite angles."""
+    return _rope(_lib.kta_rope_bwd, dq, dk, freqs, dims, begin, layout, mscale, pos, pos0, heads, out,
+                 stream)
+
+
+def _conv_args(x, w, bias, silu, S0, lens, step=False):
+    dt = _io(x, "x")
+    if x.dim() != (2 if step else 3):
+        raise ValueError("x must be [B, D]" if step else "x must be [B, L, D]")
+    B, D = x.shape[0], x.shape[-1]
+    L = 1 if step else x.shape[1]
+    if w.dim() != 2:
+        raise ValueError("w must be [D, K]")
+    K = w.shape[1]
+    _want(w, "w", torch.float32, (D, K), x)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (D,), x)
+    if S0 is not None:
+        _want(S0, "S0", x.dtype, (B, K - 1, D), x)
+    if lens is not None:
+        _want(lens, "lens", torch.int32, (B,), x)
+    return ShortConv(B, L, D, K, dt, int(silu), _at(x), _at(w), _at(bias), _at(S0), _at(lens))
+
+
+def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
+                   return_state: bool = False, out=None, stream=None):
+    """Causal convolution of x [B, L, D] (bf16 or fp32) with one filter per channel, w [D, K] fp32
+    (K = 2, 3, 4; the last tap is the token's own), bias [D] fp32, then silu. S0 [B, K-1, D]: the rows
+    before the first (zeros without). lens [B] int32: rows of each sequence; o is left alone past them
+    (fresh buffers are zero there) and the end state is taken there. Returns o (and the last K - 1
+    rows)."""
+    c = _conv_args(x, w, bias, silu, S0, lens)
+    if out is not None:
+        _want(out, "out", x.dtype, x.shape, x)
+    with _on(x, stream, (x, w, bias, S0, lens, out)) as st:
+        o = out if out is not None else torch.empty_like(x) if lens is None else torch.zeros_like(x)
+        S = torch.empty((c.B, c.K - 1, c.D), device=x.device, dtype=x.dtype) if return_state else None
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _at(o), _at(S), st), "kta_short_conv_fwd")
+    return (o, S) if return_state else o
+
+
+def short_conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, out=None,
+                    stream=None):
+    """One token: x [B, D] after the rows in state [B, K-1, D], which is moved on in place (or into
+    state_out). Returns o [B, D]."""
+    if state is None:
+        raise ValueError("state must be a tensor")
+    c = _conv_args(x, w, bias, silu, state, None, step=True)
+    if state_out is not None:
+        _want(state_out, "state_out", x.dtype, state.shape, x)
+    if out is not None:
+        _want(out, "out", x.dtype, x.shape, x)
+    with _on(x, stream, (x, w, bias, state, state_out, out)) as st:
+        o = torch.empty_like(x) if out is None else out
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _at(o),
+                                       _at(state if state_out is None else state_out), st),
+               "kta_short_conv_fwd")
+    return o
+
+
+def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=None, dS_out=None,
+                   out=None, stream=None):
+    """Gradients (dx, dw, dbias, dS0) of sum(dout * o) + sum(dS_out * S_out) of short_conv_fwd; dbias
+    and dS0 are None without bias and S0. dx is left alone past a sequence's end (a fresh buffer is
+    zero there); out = a buffer for dx."""
+    c = _conv_args(x, w, bias, silu, S0, lens)
+    _want(dout, "dout", x.dtype, x.shape, x)
+    if dS_out is not None:
+        _want(dS_out, "dS_out", x.dtype, (c.B, c.K - 1, c.D), x)
+    if out is not None:
+        _want(out, "out", x.dtype, x.shape, x)
+    with _on(x, stream, (x, w, bias, S0, lens, dout, dS_out, out)) as st:
+        dx = out if out is not None else torch.empty_like(x) if lens is None else torch.zeros_like(x)
+        dw = torch.empty_like(w)
+        dbias = None if bias is None else torch.empty_like(bias)
+        dS0 = None if S0 is None else torch.empty_like(S0)
+        ws = _scratch(n := _lib.kta_short_conv_bwd_workspace(ctypes.byref(c)), x)
+        _check(_lib.kta_short_conv_bwd(ctypes.byref(c), _at(dout), _at(dS_out), _at(dx), _at(dw),
+                                       _at(dbias), _at(dS0), _at(ws), n, st), "kta_short_conv_bwd")
+    return dx, dw, dbias, dS0
+
+
+def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, step=False):
+    ty = _io(u, "u")
+    if u.dim() != (2 if step else 3):
+        raise ValueError("u must be [B, D]" if step else "u must be [B, L, D]")
+    if A.dim() != 2 or Bm.dim() != u.dim() + 1:
+        raise ValueError("A must be [D, N], Bm and Cm [B, G, N]" if step else
+                         "A must be [D, N], Bm and Cm [B, L, G, N]")
+    Bn, C, N, G = u.shape[0], u.shape[-1], A.shape[1], Bm.shape[-2]
+    _want(dt, "dt", u.dtype, u.shape, u)
+    _want(A, "A", torch.float32, (C, N), u)
+    _want(Bm, "Bm", u.dtype, u.shape[:-1] + (G, N), u)
+    _want(Cm, "Cm", u.dtype, Bm.shape, u)
+    if D is not None:
+        _want(D, "D", torch.float32, (C,), u)
+    if z is not None:
+        _want(z, "z", u.dtype, u.shape, u)
+    if dt_bias is not None:
+        _want(dt_bias, "dt_bias", torch.float32, (C,), u)
+    if S0 is not None:
+        _want(S0, "S0", torch.float32, (Bn, C, N), u)
+    if lens is not None:
+        _want(lens, "lens", torch.int32, (Bn,), u)
+    return Ssm(Bn, 1 if step else u.shape[1], C, N, G, ty, _at(u), _at(dt), _at(A), _at(Bm), _at(Cm),
+               _at(D), _at(z), _at(dt_bias), _at(S0), _at(lens))
+
+
+def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
+                 return_state: bool = False, out=None, stream=None):
+    """Selective state-space scan of u [B, L, D] (bf16 or fp32): h_t = exp(d_t A) h_{t-1} + d_t u_t B_t
+    with d = softplus(dt + dt_bias), y = (C . h + D u) silu(z). dt, z like u; A [D, N] fp32; Bm, Cm
+    [B, L, G, N] like u, group g for channels g D/G ..; D, dt_bias [D] fp32; S0 [B, D, N] fp32. lens
+    [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
+    end state is taken there. Returns y (and the end state)."""
+    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    if out is not None:
+        _want(out, "out", u.dtype, u.shape, u)
+    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, out)) as st:
+        y = out if out is not None else torch.empty_like(u) if lens is None else torch.zeros_like(u)
+        S = torch.empty((c.B, c.D, c.N), device=u.device, dtype=torch.float32) if return_state else None
+        ws = _scratch(n := _lib.kta_ssm_scan_fwd_workspace(ctypes.byref(c)), u)
+        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), _at(y), _at(S), _at(ws), n, st),
+               "kta_ssm_scan_fwd")
+    return (y, S) if return_state else y
+
+
+def ssm_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, state_out=None, out=None,
+                  stream=None):
+    """One token of ssm_scan_fwd: u, dt, z [B, D], Bm, Cm [B, G, N]; state [B, D, N] fp32 is moved on
+    in place (or into state_out). Returns y [B, D]."""
+    if state is None:
+        raise ValueError("state must be a tensor")
+    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
+    if state_out is not None:
+        _want(state_out, "state_out", torch.float32, state.shape, u)
+    if out is not None:
+        _want(out, "out", u.dtype, u.shape, u)
+    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, state, state_out, out)) as st:
+        y = torch.empty_like(u) if out is None else out
+        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), _at(y),
+                                      _at(state if state_out is None else state_out), st),
+               "kta_ssm_scan_step")
+    return y
+
+
+def ssm_scan_bwd(u, dt, A, Bm, Cm, dout, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
+                 dS_out=None, out=None, stream=None):
+    """Gradients of sum(dout * y) + sum(dS_out * S_out) of ssm_scan_fwd, as a dict: du, ddt, dA, dB,
+    dC, and dD, dz, ddt_bias, dS0 (None where the input is). du, ddt, dz, dB, dC are left alone past a
+    sequence's end (fresh buffers are zero there); out = a dict of buffers for any of these five."""
+    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    _want(dout, "dout", u.dtype, u.shape, u)
+    if dS_out is not None:
+        _want(dS_out, "dS_out", torch.float32, (c.B, c.D, c.N), u)
+    out = {k: t for k, t in (out or {}).items() if t is not None}
+    like = {"du": u, "ddt": dt, "dz": z, "dB": Bm, "dC": Cm}
+    for n, t in out.items():
+        if like.get(n) is None:
+            raise ValueError(f"no gradient {n!r} to write into out")
+        _want(t, n, u.dtype, like[n].shape, u)
+    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, dout, dS_out,
+                         *out.values())) as st:
+        fresh = torch.empty_like if lens is None else torch.zeros_like
+        g = {n: None if t is None else out[n] if n in out else fresh(t) for n, t in like.items()}
+        for n, t in (("dA", A), ("dD", D), ("ddt_bias", dt_bias), ("dS0", S0)):
+            g[n] = None if t is None else torch.empty_like(t)
+        ws = _scratch(n := _lib.kta_ssm_scan_bwd_workspace(ctypes.byref(c)), u)
+        grads = SsmGrads(_at(dout), _at(dS_out), _at(g["du"]), _at(g["ddt"]), _at(g["dA"]),
+                         _at(g["dB"]), _at(g["dC"]), _at(g["dD"]), _at(g["dz"]), _at(g["ddt_bias"]),
+                         _at(g["dS0"]))
+        _check(_lib.kta_ssm_scan_bwd(ctypes.byref(c), ctypes.byref(grads), _at(ws), n, st),
+               "kta_ssm_scan_bwd")
+    return g
 
 
 def device_status(stream=None):

@@ -375,6 +375,153 @@ kta_status kta_stream_load(kta_stream_t st, const void* dev_src, void* stream);
 kta_status kta_stream_destroy(kta_stream_t st);
 
 /*
+ * Rotary positions of softmax heads -- the pages give SWA and DSWA as standard attention and say
+ * nothing of positions; this is the rotation such heads take before it. Dims [begin, begin + rot)
+ * of every head (rot = sum of dims) are cut into one section per position axis (e.g. frame, row,
+ * column), axis 0 first. Pair i of a section turns by t = pos_axis * freq_i:
+ *     (a, b) -> mscale (a cos t - b sin t, a sin t + b cos t),
+ * with (a, b) = dims (j, j + dims/2) of the section (interleaved = 0) or (2j, 2j + 1)
+ * (interleaved = 1). The other dims of the head are copied, bit for bit (with o = x: left alone).
+ *  - pos: [N][n_axes] int64, or [B][N][n_axes] with pos_per_seq = 1, device, 8-byte aligned; NULL
+ *    (one axis only) = the token's place in its sequence. pos0 is added to axis 0's position (the
+ *    frame or token a rollout has reached). Angles are formed in 64 bits and reduced to one turn
+ *    before they are rounded: |pos| <= 2^31 keeps them within 2^-20 of exact.
+ *  - freqs: radians per position, one double per pair, device, 8-byte aligned (kta_rope_freqs).
+ *  - x, o: [B][N][ld_heads][d], H heads, as everywhere; x2, o2: a second tensor of the same B, N, d
+ *    and dtype with H2 heads of ld_heads2 (keys beside queries), or both NULL (H2, ld_heads2 then
+ *    ignored). Products and sums are fp32, rounded once.
+ *  - o = x (and o2 = x2) rotates in place; no other overlap.
+ *  - dims[] even, >= 2; begin even; begin + rot <= d.
+ * kta_rope_bwd is the gradient: the rotation by -t (scaled by mscale) of dout.
+ */
+typedef struct {
+  int n_axes;               /* 1..4 */
+  int dims[4];              /* dims of each axis' section */
+  int begin;                /* first dim that turns */
+  int interleaved;
+  float mscale;             /* 1 unless the frequencies were scaled by parts */
+  const int64_t* pos;
+  int pos_per_seq;
+  int64_t pos0;
+  const double* freqs;
+} kta_rope;
+
+kta_status kta_rope_fwd(const kta_rope* cfg, const void* x, void* o, const void* x2, void* o2,
+                        kta_shape s, int H, int ld_heads, int H2, int ld_heads2, void* stream);
+kta_status kta_rope_bwd(const kta_rope* cfg, const void* dout, void* dx, const void* dout2, void* dx2,
+                        kta_shape s, int H, int ld_heads, int H2, int ld_heads2, void* stream);
+
+/*
+ * Frequencies of one section of `dims` dims, into a HOST array of dims / 2 doubles, and the scale
+ * of the rotated values. Plain: freq_i = base^(-2i/dims). For contexts `factor` times longer:
+ *   LINEAR    freq_i / factor;
+ *   BASE      base * factor^(dims/(dims-2)): the lowest frequency is divided by factor, the highest
+ *             kept ("NTK-aware");
+ *   BY_PARTS  with r_i = orig_len freq_i / 2 pi turns over the original length: freq_i where
+ *             r_i >= beta_fast, freq_i / factor where r_i <= beta_slow, a linear ramp in r_i between,
+ *             and mscale = 0.1 ln(factor) + 1 (YaRN, Peng et al. 2023). Usual betas: 32 and 1.
+ */
+typedef enum { KTA_ROPE_PLAIN = 0, KTA_ROPE_LINEAR = 1, KTA_ROPE_BASE = 2, KTA_ROPE_BY_PARTS = 3 } kta_rope_scaling;
+
+kta_status kta_rope_freqs(int dims, double base, int scaling, double factor, double orig_len,
+                          double beta_fast, double beta_slow, double* freqs, float* mscale);
+
+/*
+ * Short causal convolution -- one filter of K taps per channel along the tokens, in front of the
+ * linear heads' q, k, v or of a state-space head's input (the GatedDeltaNet block, which the
+ * paper-read's GLA paragraph names as the branch's basis, has one; the pages do not show it):
+ *     pre_t = bias + sum_{j<K} w_j x_{t-K+1+j},   o_t = silu(pre_t) (silu = 1) or pre_t.
+ *  - x, o: [B][L][D] (dtype); w: [D][K] fp32; bias: [D] fp32 or NULL. K in {2, 3, 4}; D % 8 == 0;
+ *    every pointer 16-byte aligned.
+ *  - S0: [B][K-1][D] (dtype), the K - 1 rows before the first (oldest first), or NULL = zeros.
+ *    S_out: the last K - 1 rows of [S0; x], or NULL. S_out = S0 updates the state in place; with
+ *    L = 1 this is the step of a rollout.
+ *  - lens: [B] int32 device array or NULL: sequence b has min(max(lens[b], 0), L) rows; the rows of
+ *    x after them are not read, those of o not written, and the end state is taken at their end.
+ *  - No output may overlap another tensor (but S_out = S0).
+ * kta_short_conv_bwd: dx [B][L][D] (rows past a sequence's end are left), dw [D][K], dbias [D]
+ * or NULL (fp32), dS0 [B][K-1][D] or NULL; dS_out: gradient of S_out or NULL. Sums run in a fixed
+ * order: the same call gives the same bits. ws: kta_short_conv_bwd_workspace(c) bytes of device
+ * memory, 16-byte aligned, for this call alone until it has run (0 from the query = bad arguments).
+ */
+typedef struct {
+  int B, L, D, K;
+  kta_dtype dtype;
+  int silu;
+  const void* x;
+  const float* w;
+  const float* bias;
+  const void* S0;
+  const int32_t* lens;
+} kta_short_conv;
+
+kta_status kta_short_conv_fwd(const kta_short_conv* c, void* o, void* S_out, void* stream);
+size_t kta_short_conv_bwd_workspace(const kta_short_conv* c);
+kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const void* dS_out, void* dx,
+                              float* dw, float* dbias, void* dS0, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Selective state-space scan -- a linear-recurrence head beside GLA and the delta rule, with a decay
+ * of its own for every channel and state (Gu & Dao 2023; the pages name linear recurrences with
+ * input-dependent gates and show GLA only). With d_t = softplus(dt_t + dt_bias) > 0, per sequence,
+ * channel c of group g and state n < N:
+ *     h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,   y_t = (sum_n C_t h_t + D_skip u_t) silu(z_t).
+ *  - u, dt, z, y: [B][L][D] (dtype); Bm, Cm: [B][L][G][N] (dtype), group g = c / (D / G);
+ *    A: [D][N] fp32 (negative for a decaying state; any finite value is taken); D_skip, dt_bias: [D]
+ *    fp32 or NULL (= 0); z NULL = no gate. 1 <= N <= 32; G divides D; (D / G) % 8 == 0; every
+ *    pointer 16-byte aligned, but Bm, Cm and their gradients by their element alone.
+ *  - S0, S_out: [B][D][N] fp32, the state before the first and after the last token; NULL = zero / not
+ *    wanted. States and sums are fp32; y is rounded once.
+ *  - lens: as in kta_short_conv.
+ *  - No output may overlap another tensor (but kta_ssm_scan_step's S_out = S0).
+ *  - ws: kta_ssm_scan_fwd_workspace(c) bytes (asked with the same device current; may be 0), device
+ *    memory, 16-byte aligned, for this call alone until it has run. A long sequence with few channels
+ *    is cut into segments that run at once: their end states from zero are kept there.
+ * kta_ssm_scan_step: one token (L = 1) from S0 to S_out; S_out = S0 updates in place; no workspace.
+ *
+ * kta_ssm_scan_bwd: gradients of sum(dout * y) + sum(dS_out * S_out). With dy_t = dout_t silu(z_t) and
+ * G_t = dy_t C_t + exp(d_{t+1} A) G_{t+1} (behind the last token: dS_out or 0):
+ *     dC_t = sum_c dy_t h_t,   dB_t = sum_c G_t d_t u_t,   dx_t = sum_n G_t B_t,
+ *     w_t = G_t exp(d_t A) h_{t-1},   dA = sum_t w_t d_t,   dd_t = dx_t u_t + sum_n w_t A,
+ *     du_t = dx_t d_t + D_skip dy_t,   ddt_t = dd_t sigmoid(dt_t + dt_bias),   ddt_bias = sum_t ddt_t,
+ *     dz_t = dout_t silu'(z_t) (sum_n C_t h_t + D_skip u_t),   dD_skip = sum_t dy_t u_t,   dS0 = exp(d_0 A) G_0.
+ * du, ddt, dz (with z), dB, dC: dtype and layout of their tensors, rows past a sequence's end left;
+ * dA [D][N], dD_skip, ddt_bias [D], dS0 [B][D][N]: fp32 (the last three NULL = not wanted). Nothing is
+ * kept from the forward call. Sums run in a fixed order: the same call gives the same bits.
+ */
+typedef struct {
+  int B, L, D, N, G;
+  kta_dtype dtype;
+  const void *u, *dt;
+  const float* A;
+  const void *Bm, *Cm;
+  const float* D_skip;
+  const void* z;
+  const float *dt_bias, *S0;
+  const int32_t* lens;
+} kta_ssm;
+
+typedef struct {
+  const void* dout;
+  const float* dS_out;
+  void *du, *ddt;
+  float* dA;
+  void *dB, *dC;
+  float* dD_skip;
+  void* dz;
+  float *ddt_bias, *dS0;
+} kta_ssm_grads;
+
+size_t kta_ssm_scan_fwd_workspace(const kta_ssm* c);
+kta_status kta_ssm_scan_fwd(const kta_ssm* c, void* y, float* S_out, void* ws, size_t ws_bytes,
+                            void* stream);
+kta_status kta_ssm_scan_step(const kta_ssm* c, void* y, float* S_out, void* stream);
+size_t kta_ssm_scan_bwd_workspace(const kta_ssm* c);
+kta_status kta_ssm_scan_bwd(const kta_ssm* c, const kta_ssm_grads* g, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
  * Device-side health. Every wait inside the library's kernels is bounded; a wait that runs out
  * records a code in a device error word and lets its kernel finish cleanly instead of hanging.
  * kta_device_status synchronises `stream`, returns KTA_ERR_TIMEOUT if such a code was recorded
