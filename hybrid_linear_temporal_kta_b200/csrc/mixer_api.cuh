@@ -324,46 +324,66 @@ kta::SsmParams ssm_params(const kta_ssm* c) {
   p.G = c->G;
   p.Dg = c->D / c->G;
   p.cbg = (p.Dg + kta::SSM_CH - 1) / kta::SSM_CH;
-  p.bc_vec = static_cast<size_t>(c->N) * elem_size(c->dtype) % 16 == 0 && aligned16(c->Bm) && aligned16(c->Cm);
+  const uintptr_t bc = static_cast<uintptr_t>(c->N) * elem_size(c->dtype) |
+                       reinterpret_cast<uintptr_t>(c->Bm) | reinterpret_cast<uintptr_t>(c->Cm);
+  p.bc_bytes = bc % 16 == 0 ? 16 : bc % 8 == 0 ? 8 : bc % 4 == 0 ? 4 : 0;
   return p;
 }
 
 // States per lane: the smallest power of two that holds N in four lanes.
 int ssm_ns(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 
-// Segments of the forward pass.
+// States a lane of the forward pass holds: the power of two, at least 4, that holds N.
+int ssm_np(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : 32; }
+
+// Segments of the forward pass. Every exponential of a segment but the last is computed twice (end
+// state, then outputs), so a sequence stays whole once its warps give each of the SM's four
+// schedulers one (B 8, D 4,096, N 16: 551 us whole, 660 in two); with fewer, segments fill the four
+// warps that fit on each (B 4, L 2,048, D 2,048: 475 us whole, 202 in nine). A segment shorter
+// than 64 tokens costs more to start than it gains.
 void ssm_plan(kta::SsmParams& p) {
-  const long long blocks = static_cast<long long>(p.B) * p.G * p.cbg;
-  long long n = 1;
-  if (blocks < 2LL * sm_count()) {
-    n = (4LL * sm_count() + blocks - 1) / blocks;
-    n = std::min<long long>(n, p.L / (4 * kta::SSM_TT));
-    n = std::max<long long>(1, std::min<long long>(n, 64));
-  }
+  const long long warps = static_cast<long long>(p.B) * p.G * p.cbg;
+  const long long one = 4LL * sm_count(), full = one * (ssm_np(p.N) > 16 ? 3 : 4);
+  long long n = warps >= one ? 1 : std::max<long long>(1, std::min<long long>(full / warps, p.L / 64));
   p.seg = static_cast<int>((p.L + n - 1) / n);
   p.seg = (p.seg + kta::SSM_TT - 1) / kta::SSM_TT * kta::SSM_TT;
   p.nseg = (p.L + p.seg - 1) / p.seg;
 }
 
-size_t ssm_fwd_bytes(const kta::SsmParams& p) {
-  if (p.nseg == 1) return 0;
-  const size_t rows = static_cast<size_t>(p.B) * p.nseg * p.D;
-  return mixer_round(rows * p.N * 4) + mixer_round(rows * 4);
+size_t ssm_fwd_states_bytes(const kta::SsmParams& p) {
+  return mixer_round(static_cast<size_t>(p.B) * p.nseg * p.D * ssm_np(p.N) * 4);
 }
 
-template <typename T, int NS>
+size_t ssm_fwd_bytes(const kta::SsmParams& p) {
+  return p.nseg == 1 ? 0 : ssm_fwd_states_bytes(p) + mixer_round(static_cast<size_t>(p.B) * p.nseg * p.D * 4);
+}
+
+template <typename T, int NP>
 kta_status launch_ssm_fwd(const kta::SsmParams& p, cudaStream_t st) {
+  constexpr int W = kta::SSM_THREADS / 32;
   const long long per = static_cast<long long>(p.B) * p.G * p.cbg;
+  const long long states = static_cast<long long>(p.B) * p.D * NP;
+  const size_t smem_out = W * sizeof(kta::SsmFwdSmem<T, NP, true>);
+  const size_t smem_loc = W * sizeof(kta::SsmFwdSmem<T, NP, false>);
   kta_status r;
-  if ((r = check_grid(per * p.nseg))) return r;
+  if ((r = check_grid((per * p.nseg + W - 1) / W)) || (r = check_grid((states + 255) / 256)) ||
+      (r = set_smem_attr(kta::ssm_fwd_kernel<T, NP, true>, smem_out)))
+    return r;
   if (p.nseg > 1) {
-    TraceScope ts("ssm_local", st);
-    kta::ssm_fwd_kernel<T, NS, false>
-        <<<static_cast<unsigned>(per * (p.nseg - 1)), kta::SSM_THREADS, 0, st>>>(p);
+    if ((r = set_smem_attr(kta::ssm_fwd_kernel<T, NP, false>, smem_loc))) return r;
+    {
+      TraceScope ts("ssm_local", st);
+      kta::ssm_fwd_kernel<T, NP, false>
+          <<<static_cast<unsigned>((per * (p.nseg - 1) + W - 1) / W), kta::SSM_THREADS, smem_loc, st>>>(p);
+      KTA_CUDA(cudaGetLastError());
+    }
+    TraceScope ts("ssm_carry", st);
+    kta::ssm_fwd_carry_kernel<<<static_cast<unsigned>((states + 255) / 256), 256, 0, st>>>(p, NP);
     KTA_CUDA(cudaGetLastError());
   }
   TraceScope ts("ssm_fwd", st);
-  kta::ssm_fwd_kernel<T, NS, true><<<static_cast<unsigned>(per * p.nseg), kta::SSM_THREADS, 0, st>>>(p);
+  kta::ssm_fwd_kernel<T, NP, true>
+      <<<static_cast<unsigned>((per * p.nseg + W - 1) / W), kta::SSM_THREADS, smem_out, st>>>(p);
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }
@@ -447,6 +467,21 @@ kta_status launch_ssm_bwd(const kta::SsmBwdParams& p, cudaStream_t st) {
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }
+
+#define KTA_SSM_FWD_DISPATCH(fn, dtype, N, ...)                                 \
+  do {                                                                          \
+    const int np_ = ssm_np(N);                                                  \
+    if ((dtype) == KTA_BF16) {                                                  \
+      if (np_ == 4) return fn<__nv_bfloat16, 4>(__VA_ARGS__);                   \
+      if (np_ == 8) return fn<__nv_bfloat16, 8>(__VA_ARGS__);                   \
+      if (np_ == 16) return fn<__nv_bfloat16, 16>(__VA_ARGS__);                 \
+      return fn<__nv_bfloat16, 32>(__VA_ARGS__);                                \
+    }                                                                           \
+    if (np_ == 4) return fn<float, 4>(__VA_ARGS__);                             \
+    if (np_ == 8) return fn<float, 8>(__VA_ARGS__);                             \
+    if (np_ == 16) return fn<float, 16>(__VA_ARGS__);                           \
+    return fn<float, 32>(__VA_ARGS__);                                          \
+  } while (0)
 
 #define KTA_SSM_DISPATCH(fn, dtype, N, ...)                                     \
   do {                                                                          \
@@ -588,11 +623,10 @@ kta_status kta_ssm_scan_fwd(const kta_ssm* c, void* y, float* S_out, void* ws, s
   p.S_out = S_out;
   if (need) {
     p.seg_h = static_cast<float*>(ws);
-    p.seg_d = reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                       mixer_round(static_cast<size_t>(p.B) * p.nseg * p.D * p.N * 4));
+    p.seg_d = reinterpret_cast<float*>(static_cast<char*>(ws) + ssm_fwd_states_bytes(p));
   }
   cudaStream_t st = as_stream(stream);
-  KTA_SSM_DISPATCH(launch_ssm_fwd, c->dtype, c->N, p, st);
+  KTA_SSM_FWD_DISPATCH(launch_ssm_fwd, c->dtype, c->N, p, st);
 }
 
 kta_status kta_ssm_scan_step(const kta_ssm* c, void* y, float* S_out, void* stream) {

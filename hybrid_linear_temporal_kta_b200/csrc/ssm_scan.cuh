@@ -3,23 +3,16 @@
 //     h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,    y_t = (C_t . h_t + Dskip u_t) silu(z_t),
 // B and C shared by the channels of a group. States, gates and sums are fp32.
 //
-// Layout: a warp holds 8 channels x 4 state quarters; a lane keeps NS = ceil(N / 4) states of one
-// channel in registers (NS a power of two, states past N are zero) and a block 32 channels. Tokens
-// come in tiles of SSM_TT: the block turns dt and u into (d, d u) pairs once per (token, channel)
-// and B, C into fp32 rows in shared memory, every lane walks the tile, the four partial sums of y
-// are joined by halving exchanges, and whole 16-byte rows are gated and stored.
-//
-// Bound by the exponential: one per (token, channel, state), 16 a clock per SM, against 8 bytes per
-// (token, channel) in bf16.
+// Bound by the exponential unit: one exponential per (token, channel, state), a warp's 32 in 8 cycles
+// of its scheduler, against 8 bytes per (token, channel) in bf16.
 #pragma once
 #include "mixer_common.cuh"
 
 namespace kta {
 
 constexpr int SSM_THREADS = 128;
-constexpr int SSM_CH = 32;      // channels per block
-constexpr int SSM_TT = 32;      // tokens per tile (forward)
-constexpr int SSM_GRP = 8;      // tokens whose outputs are joined at once (forward)
+constexpr int SSM_CH = 32;      // channels per warp (forward) or block (backward)
+constexpr int SSM_TT = 8;       // tokens per tile (forward)
 constexpr int SSM_MAX_N = 32;
 
 struct SsmParams {
@@ -31,8 +24,8 @@ struct SsmParams {
   int B, L, D, N, G, Dg;         // Dg = D / G channels per group
   int cbg;                       // channel blocks per group
   int nseg, seg;                 // segments of the sequence and their tokens (a multiple of SSM_TT)
-  int bc_vec;                    // rows of B and C may be read as 16-byte pieces
-  float *seg_h, *seg_d;          // [B][nseg][D][N] end states from zero, [B][nseg][D] sums of d
+  int bc_bytes;                  // rows of B and C may be read in pieces of 16, 8 or 4 bytes; 0: elements
+  float *seg_h, *seg_d;          // end states of segments from zero, sums of d
 };
 
 struct SsmBlock {
@@ -101,7 +94,7 @@ __device__ __forceinline__ void ssm_stage_bc(const SsmParams& p, const void* src
   const T* rows = static_cast<const T*>(src);
   const long long ld = static_cast<long long>(p.G) * p.N;
   const long long r0 = (static_cast<long long>(b) * p.L + t0) * ld + g * p.N;
-  if (p.bc_vec) {
+  if (p.bc_bytes == 16) {
     const int nv = p.N / V;
     for (int i = threadIdx.x; i < TT * nv; i += SSM_THREADS) {
       const int t = i / nv, v = i - t * nv;
@@ -119,148 +112,262 @@ __device__ __forceinline__ void ssm_stage_bc(const SsmParams& p, const void* src
   }
 }
 
-// OUT: outputs (and, past the last segment, the end state) from the state that enters the segment,
-// folded from the segments before it. Otherwise: the segment's end state from zero and its sum of d.
-template <typename T, int NS, bool OUT>
-__global__ __launch_bounds__(SSM_THREADS) void ssm_fwd_kernel(const SsmParams p) {
-  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, ITEMS = SSM_TT * CPR / SSM_THREADS;
-  __shared__ __align__(16) float2 s_d[SSM_TT][SSM_CH];          // d, d u
-  __shared__ __align__(16) float s_b[SSM_TT * 4 * NS];
-  __shared__ __align__(16) float s_c[OUT ? SSM_TT * 4 * NS : 4];
-  __shared__ __align__(16) float s_y[OUT ? SSM_TT : 1][SSM_CH + 4];
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, q = lane % 4;
-  const SsmBlock k = ssm_block(p, blockIdx.x, OUT ? p.nseg : p.nseg - 1);
-  const int ch = warp * 8 + lane / 4;                  // channel in the block
-  const bool live = ch < k.cw;
-  const long long c = k.c0 + (live ? ch : 0);
+// Forward. A warp takes 32 channels of a group over one segment, a lane all states of one channel: rows
+// of B and C are then the same for the whole warp (broadcast reads), and lanes exchange nothing. Raw
+// tiles of 8 tokens arrive by asynchronous copies, two (fp32: one) ahead; a lane turns its channel's dt
+// and u into (d, d u) for the tile, walks the tokens with its states in registers as packed pairs, gates
+// the 8 outputs, and the tile leaves as 16-byte rows. Warps of a block share nothing; blocks have four so
+// that each scheduler of the SM gets one. 128 registers keep 4 warps on a scheduler, which hide each
+// other's exponentials: 206 cycles a token and warp against the unit's 152.
+//
+// (Four lanes per channel with the sum over states exchanged between them needed twice the
+// instructions and shared-memory reads per token: 1.3 times the time. Computing one exponential in four
+// or eight on the FMA pipe by a polynomial gained nothing: the issue slots are as short.)
+template <typename T, int NP, bool OUT>
+struct SsmFwdSmem {
+  static constexpr int STAGES = sizeof(T) == 2 ? 3 : 2;
+  struct Raw {                             // every part is the target of 16-byte copies
+    alignas(16) T u[SSM_TT][SSM_CH];
+    alignas(16) T d[SSM_TT][SSM_CH];
+    alignas(16) T z[OUT ? SSM_TT : 1][SSM_CH];
+    alignas(16) T b[SSM_TT][NP];
+    alignas(16) T c[OUT ? SSM_TT : 1][NP];
+  };
+  Raw raw[STAGES];
+  alignas(16) float bc[SSM_TT][OUT ? 2 : 1][NP];   // rows of B (and C) of the current tile, fp32
+  alignas(16) float2 dd[SSM_TT][SSM_CH];           // d, d u; then (x) the token's C . h
+};
+
+static_assert(sizeof(SsmFwdSmem<__nv_bfloat16, 4, false>) % 16 == 0 &&
+                  sizeof(SsmFwdSmem<__nv_bfloat16, 4, false>::Raw) % 16 == 0,
+              "warps' and stages' parts stay 16-byte aligned");
+
+// One piece size of a tile's rows of B and C.
+template <typename T, int NP, bool OUT, int BYTES, typename Raw>
+__device__ __forceinline__ void ssm_fetch_bc(const SsmParams& p, Raw& r, long long row0, int g, int t0, int t_end,
+                                             int lane) {
+  constexpr int V = BYTES / int(sizeof(T)) > 0 ? BYTES / int(sizeof(T)) : 1, NV = (NP + V - 1) / V;
+#pragma unroll
+  for (int m = 0; m < (SSM_TT * NV + 31) / 32; ++m) {
+    const int it = lane + m * 32, t = it / NV, n = it % NV * V;
+    if (it < SSM_TT * NV && n < p.N) {
+      const bool on = t0 + t < t_end;
+      const long long at = on ? ((row0 + t0 + t) * p.G + g) * p.N + n : 0;
+      piece_async<BYTES>(&r.b[t][n], static_cast<const T*>(p.Bm) + at, on);
+      if (OUT) piece_async<BYTES>(&r.c[t][n], static_cast<const T*>(p.Cm) + at, on);
+    }
+  }
+}
+
+// OUT: outputs (and, past the last segment, the end state) from the state that enters the segment.
+// Otherwise: the segment's end state from zero (seg_h [B][nseg][NP][D]) and its sum of d.
+template <typename T, int NP, bool OUT>
+__global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(const SsmParams p) {
+  using Smem = SsmFwdSmem<T, NP, OUT>;
+  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, STAGES = Smem::STAGES;
+  extern __shared__ __align__(16) unsigned char ssm_smem[];
+  Smem& sm = reinterpret_cast<Smem*>(ssm_smem)[threadIdx.x / 32];
+  const int lane = threadIdx.x % 32;
+  const int nseg = OUT ? p.nseg : p.nseg - 1;
+  const long long wid = blockIdx.x * static_cast<long long>(SSM_THREADS / 32) + threadIdx.x / 32;
+  if (wid >= static_cast<long long>(p.B) * nseg * p.G * p.cbg) return;
+  const SsmBlock k = ssm_block(p, wid, nseg);
+  const bool live = lane < k.cw;
+  const int c = k.c0 + (live ? lane : 0);
   const int len = seq_len(p.lens, k.b, p.L);
   const int t_begin = k.s * p.seg, t_end = min(t_begin + p.seg, len);
-  const long long state = (static_cast<long long>(k.b) * p.D + c) * p.N;
+  const long long row0 = static_cast<long long>(k.b) * p.L;
 
-  float A2[NS], h[NS];
-  ssm_load_states<NS>(p.A + c * p.N, q, p.N, A2);
+  auto fetch = [&](int t0, int stage) {
+    typename Smem::Raw& r = sm.raw[stage];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    A2[i] *= 1.4426950408889634f;
-    h[i] = 0.f;
-  }
-  if (OUT) {
-    if (p.S0) ssm_load_states<NS>(p.S0 + state, q, p.N, h);
-    for (int s = 0; s < k.s; ++s) {
-      const long long r = (static_cast<long long>(k.b) * p.nseg + s) * p.D + c;
-      float e[NS];
-      ssm_load_states<NS>(p.seg_h + r * p.N, q, p.N, e);
-      const float sd = p.seg_d[r];
-#pragma unroll
-      for (int i = 0; i < NS; ++i) h[i] = fmaf(ex2_approx(sd * A2[i]), h[i], e[i]);
+    for (int m = 0; m < SSM_TT * CPR / 32; ++m) {
+      const int it = lane + m * 32, t = it / CPR, cc = it % CPR * V;
+      const bool on = t0 + t < t_end && cc < k.cw;
+      const long long at = on ? (row0 + t0 + t) * p.D + k.c0 + cc : 0;
+      piece_async<16>(&r.u[t][cc], static_cast<const T*>(p.u) + at, on);
+      piece_async<16>(&r.d[t][cc], static_cast<const T*>(p.dt) + at, on);
+      if (OUT && p.z) piece_async<16>(&r.z[t][cc], static_cast<const T*>(p.z) + at, on);
     }
-  }
-  // states past N stay zero: their columns of B and C are
-  for (int i = tid; i < SSM_TT * 4 * NS; i += SSM_THREADS) {
-    s_b[i] = 0.f;
-    if (OUT) s_c[i] = 0.f;
-  }
-  float sum_d = 0.f;
-
-  // raw rows of the current tile, one (token, 16-byte piece) per thread and item
-  VecPack<T, V> ru[ITEMS], rd[ITEMS], rz[ITEMS];
-  auto load_tile = [&](int t0) {
-#pragma unroll
-    for (int m = 0; m < ITEMS; ++m) {
-      const int it = tid + m * SSM_THREADS, t = t0 + it / CPR, cc = it % CPR * V;
-      if (t < t_end && cc < k.cw) {
-        const long long at = (static_cast<long long>(k.b) * p.L + t) * p.D + k.c0 + cc;
-        ru[m].load(static_cast<const T*>(p.u) + at);
-        rd[m].load(static_cast<const T*>(p.dt) + at);
-        if (OUT && p.z) rz[m].load(static_cast<const T*>(p.z) + at);
-      }
-    }
+    if (p.bc_bytes == 16)
+      ssm_fetch_bc<T, NP, OUT, 16>(p, r, row0, k.g, t0, t_end, lane);
+    else if (p.bc_bytes == 8)
+      ssm_fetch_bc<T, NP, OUT, 8>(p, r, row0, k.g, t0, t_end, lane);
+    else if (p.bc_bytes == 4)
+      ssm_fetch_bc<T, NP, OUT, 4>(p, r, row0, k.g, t0, t_end, lane);
+    piece_commit();
   };
-  float bias[V], skip[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int cc = tid % CPR * V + i;                    // the same piece for every item
-    bias[i] = p.dt_bias && cc < k.cw ? p.dt_bias[k.c0 + cc] : 0.f;
-    skip[i] = OUT && p.Dskip && cc < k.cw ? p.Dskip[k.c0 + cc] : 0.f;
+  for (int s = 0; s < STAGES - 1; ++s) fetch(t_begin + s * SSM_TT, s);
+
+  float2 A2[NP / 2], h[NP / 2];                          // pairs of states; zero past N
+  const float* Arow = p.A + static_cast<long long>(c) * p.N;
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) {
+    A2[i].x = 2 * i < p.N ? Arow[2 * i] * 1.4426950408889634f : 0.f;
+    A2[i].y = 2 * i + 1 < p.N ? Arow[2 * i + 1] * 1.4426950408889634f : 0.f;
+    h[i] = make_float2(0.f, 0.f);
   }
-  load_tile(t_begin);
+  if (OUT && p.nseg > 1) {                               // entering states, left by ssm_fwd_carry
+    const float* s = p.seg_h + (static_cast<long long>(k.b) * p.nseg + k.s) * NP * p.D + c;
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      h[i].x = s[static_cast<long long>(2 * i) * p.D];
+      h[i].y = s[static_cast<long long>(2 * i + 1) * p.D];
+    }
+  } else if (OUT && p.S0) {
+    const float* s = p.S0 + (static_cast<long long>(k.b) * p.D + c) * p.N;
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      h[i].x = 2 * i < p.N ? s[2 * i] : 0.f;
+      h[i].y = 2 * i + 1 < p.N ? s[2 * i + 1] : 0.f;
+    }
+  }
+  for (int i = lane; i < SSM_TT * (OUT ? 2 : 1) * NP; i += 32) (&sm.bc[0][0][0])[i] = 0.f;
+
+  const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = OUT && p.Dskip ? p.Dskip[c] : 0.f;
+  float sum_d = 0.f;
+  int stage = 0;
   for (int t0 = t_begin; t0 < t_end; t0 += SSM_TT) {
-    __syncthreads();                                     // the tile before is done with
-    ssm_stage_bc<T, NS, SSM_TT>(p, p.Bm, k.b, k.g, t0, t_end, s_b);
-    if (OUT) ssm_stage_bc<T, NS, SSM_TT>(p, p.Cm, k.b, k.g, t0, t_end, s_c);
-    VecPack<T, V> cu[ITEMS], cz[ITEMS];
+    piece_wait<STAGES - 2>();
+    __syncwarp();                                        // every lane's pieces are there; dd, bc are free
+    typename Smem::Raw& r = sm.raw[stage];
 #pragma unroll
-    for (int m = 0; m < ITEMS; ++m) {
-      const int it = tid + m * SSM_THREADS, t = it / CPR, cc = it % CPR * V;
-      cu[m] = ru[m];
-      cz[m] = rz[m];
+    for (int j = 0; j < SSM_TT; ++j) {                   // past the end d = 0: the state stays
+      float d = softplus_f32(to_f32(r.d[j][lane]) + bias);
+      d = t0 + j < t_end ? d : 0.f;
+      if (!OUT) sum_d += d;
+      sm.dd[j][lane] = make_float2(d, d * to_f32(r.u[j][lane]));
+    }
+    if (p.bc_bytes) {
+      constexpr int NQ = NP / 4;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float2 v = make_float2(0.f, 0.f);                // past the end: the state stays
-        if (t0 + t < t_end && cc < k.cw) {
-          v.x = softplus_f32(to_f32(rd[m].e[i]) + bias[i]);
-          v.y = v.x * to_f32(ru[m].e[i]);
+      for (int m = 0; m < (SSM_TT * NQ + 31) / 32; ++m) {
+        const int it = lane + m * 32, t = it / NQ, n = it % NQ * 4;
+        if (it < SSM_TT * NQ && n < p.N) {
+#pragma unroll
+          for (int w = 0; w < (OUT ? 2 : 1); ++w) {
+            VecPack<T, 4> x;
+            x.load(w ? &r.c[OUT ? t : 0][n] : &r.b[t][n]);
+            float4 f = make_float4(to_f32(x.e[0]), to_f32(x.e[1]), to_f32(x.e[2]), to_f32(x.e[3]));
+            if (n + 4 > p.N) {                           // the row ends inside the quad
+              f.y = n + 1 < p.N ? f.y : 0.f;
+              f.z = n + 2 < p.N ? f.z : 0.f;
+              f.w = 0.f;
+            }
+            *reinterpret_cast<float4*>(&sm.bc[t][w][n]) = f;
+          }
         }
-        s_d[t][cc + i] = v;
+      }
+    } else {                                             // an odd row of 2-byte elements
+      for (int it = lane; it < SSM_TT * p.N; it += 32) {
+        const int t = it / p.N, n = it - t * p.N;
+        const bool on = t0 + t < t_end;
+        const long long at = on ? ((row0 + t0 + t) * p.G + k.g) * p.N + n : 0;
+        sm.bc[t][0][n] = on ? to_f32(static_cast<const T*>(p.Bm)[at]) : 0.f;
+        if (OUT) sm.bc[t][OUT ? 1 : 0][n] = on ? to_f32(static_cast<const T*>(p.Cm)[at]) : 0.f;
       }
     }
-    __syncthreads();
-    load_tile(t0 + SSM_TT);
-#pragma unroll 1
-    for (int g = 0; g < SSM_TT; g += SSM_GRP) {
-      float py[SSM_GRP];
+    __syncwarp();
+    fetch(t0 + (STAGES - 1) * SSM_TT, stage == 0 ? STAGES - 1 : stage - 1);   // into the tile before's place
 #pragma unroll
-      for (int j = 0; j < SSM_GRP; ++j) {
-        const float2 d = s_d[g + j][ch];
-        float bv[NS], cv[NS];
-        lds_states<NS>(s_b + (g + j) * 4 * NS + q * NS, bv);
-        if (OUT) lds_states<NS>(s_c + (g + j) * 4 * NS + q * NS, cv);
-        if (!OUT) sum_d += d.x;
-        py[j] = 0.f;
+    for (int j = 0; j < SSM_TT; ++j) {
+      const float2 dd = sm.dd[j][lane];
+      const uint64_t d2 = f32x2_pack(dd.x, dd.x), du2 = f32x2_pack(dd.y, dd.y);
+      uint64_t acc[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          h[i] = fmaf(ex2_approx(d.x * A2[i]), h[i], d.y * bv[i]);
-          if (OUT) py[j] = fmaf(h[i], cv[i], py[j]);
+      for (int i = 0; i < NP / 2; i += 2) {
+        const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(&sm.bc[j][0][2 * i]);
+        ulonglong2 c4;
+        if (OUT) c4 = *reinterpret_cast<const ulonglong2*>(&sm.bc[j][OUT ? 1 : 0][2 * i]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 x = f32x2_unpack(fmul2(d2, f32x2_pack(A2[i + e])));
+          const uint64_t a = f32x2_pack(ex2_approx(x.x), ex2_approx(x.y));
+          const uint64_t hn = ffma2(a, f32x2_pack(h[i + e]), fmul2(du2, e ? b4.y : b4.x));
+          h[i + e] = f32x2_unpack(hn);
+          if (OUT) acc[e] = ffma2(hn, e ? c4.y : c4.x, acc[e]);
         }
       }
       if (OUT) {
-        halve_sum(py, 8, 2, q & 2);
-        halve_sum(py, 4, 1, q & 1);
-        s_y[g + 2 * q][ch] = py[0];                      // lane q keeps tokens 2 q, 2 q + 1
-        s_y[g + 2 * q + 1][ch] = py[1];
+        const float2 y = f32x2_unpack(fadd2(acc[0], acc[1]));
+        sm.dd[j][lane].x = y.x + y.y;
       }
     }
     if (OUT) {
-      __syncthreads();
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int it = tid + m * SSM_THREADS, t = it / CPR, cc = it % CPR * V;
-        if (t0 + t < t_end && cc < k.cw) {
-          VecPack<T, V> o;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float y = fmaf(skip[i], to_f32(cu[m].e[i]), s_y[t][cc + i]);
-            if (p.z) {
-              const float z = to_f32(cz[m].e[i]);
-              y *= z * sigmoid_f32(z);
-            }
-            o.e[i] = from_f32<T>(y);
-          }
-          o.store(static_cast<T*>(p.y) + (static_cast<long long>(k.b) * p.L + t0 + t) * p.D + k.c0 + cc);
+      for (int j = 0; j < SSM_TT; ++j) {                 // the outputs take the place of u
+        float y = fmaf(skip, to_f32(r.u[j][lane]), sm.dd[j][lane].x);
+        if (p.z) {
+          const float z = to_f32(r.z[j][lane]);
+          y *= z * sigmoid_f32(z);
         }
+        r.u[j][lane] = from_f32<T>(y);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int m = 0; m < SSM_TT * CPR / 32; ++m) {
+        const int it = lane + m * 32, t = it / CPR, cc = it % CPR * V;
+        if (t0 + t < t_end && cc < k.cw)
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + (row0 + t0 + t) * p.D + k.c0 + cc) =
+              *reinterpret_cast<const uint4*>(&r.u[t][cc]);
       }
     }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
   }
   if (!live) return;
-  float* dst = nullptr;
   if (OUT) {
-    if (p.S_out && k.s == p.nseg - 1) dst = p.S_out + state;
+    if (p.S_out && k.s == p.nseg - 1) {
+      float* s = p.S_out + (static_cast<long long>(k.b) * p.D + c) * p.N;
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        if (2 * i < p.N) s[2 * i] = h[i].x;
+        if (2 * i + 1 < p.N) s[2 * i + 1] = h[i].y;
+      }
+    }
   } else {
-    const long long r = (static_cast<long long>(k.b) * p.nseg + k.s) * p.D + c;
-    dst = p.seg_h + r * p.N;
-    if (q == 0) p.seg_d[r] = sum_d;
+    const long long r = static_cast<long long>(k.b) * p.nseg + k.s;
+    float* s = p.seg_h + r * NP * p.D + c;
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      s[static_cast<long long>(2 * i) * p.D] = h[i].x;
+      s[static_cast<long long>(2 * i + 1) * p.D] = h[i].y;
+    }
+    p.seg_d[r * p.D + c] = sum_d;
   }
-  if (dst) ssm_store_states<NS>(dst, q, p.N, h);
+}
+
+// One thread per (sequence, state, channel): in place, end states of segments from zero become the
+// states that enter them. Loads of SSM_CARRY_UNROLL segments are in flight at once.
+constexpr int SSM_CARRY_UNROLL = 8;
+
+__global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, int NP) {
+  const long long per = static_cast<long long>(p.D) * NP;
+  const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (gid >= per * p.B) return;
+  const int b = static_cast<int>(gid / per);
+  const int n = static_cast<int>(gid % per / p.D), c = static_cast<int>(gid % p.D);
+  const long long e = static_cast<long long>(c) * p.N + n;
+  const bool on = n < p.N;
+  const float A2 = on ? p.A[e] * 1.4426950408889634f : 0.f;
+  float h = on && p.S0 ? p.S0[static_cast<long long>(b) * p.D * p.N + e] : 0.f;
+  float* hs = p.seg_h + (static_cast<long long>(b) * p.nseg * NP + n) * p.D + c;
+  const float* ds = p.seg_d + static_cast<long long>(b) * p.nseg * p.D + c;
+  for (int s0 = 0; s0 < p.nseg; s0 += SSM_CARRY_UNROLL) {
+    float v[SSM_CARRY_UNROLL], d[SSM_CARRY_UNROLL];
+#pragma unroll
+    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
+      if (s0 + i < p.nseg - 1) {
+        v[i] = hs[(s0 + i) * per];
+        d[i] = ds[static_cast<long long>(s0 + i) * p.D];
+      }
+#pragma unroll
+    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
+      if (s0 + i < p.nseg) {
+        hs[(s0 + i) * per] = h;
+        if (s0 + i < p.nseg - 1) h = fmaf(ex2_approx(d[i] * A2), h, v[i]);
+      }
+  }
 }
 
 // One token: memory-bound, the state read and written once (8 bytes per state against 8 per channel
@@ -276,7 +383,7 @@ __global__ __launch_bounds__(SSM_THREADS) void ssm_step_kernel(const SsmParams p
   const int c = static_cast<int>(item % p.D), g = c / p.Dg;
   if (b0 >= p.B) return;
   const int nb = min(SSM_STEP_B, p.B - b0);
-  const bool vec = NS % 4 == 0 && p.N == 4 * NS && p.bc_vec;
+  const bool vec = NS % 4 == 0 && p.N == 4 * NS && p.bc_bytes == 16;
   float h[SSM_STEP_B][NS], bv[SSM_STEP_B][NS], cv[SSM_STEP_B][NS], u[SSM_STEP_B], d[SSM_STEP_B], z[SSM_STEP_B];
 #pragma unroll
   for (int j = 0; j < SSM_STEP_B; ++j) {
@@ -461,8 +568,6 @@ __global__ __launch_bounds__(SSM_THREADS) void ssm_bwd_local_kernel(const SsmBwd
 
 // One thread per (sequence, channel, state): in place, local end states become entering states and
 // local adjoints become the adjoints entering from behind.
-constexpr int SSM_CARRY_UNROLL = 8;
-
 __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p) {
   const long long per = static_cast<long long>(p.f.D) * p.f.N;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -512,9 +617,10 @@ __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p
 template <typename T, int NS>
 struct SsmBwdSmem {
   using Cfg = SsmBwdCfg<NS>;
-  float2 d[Cfg::SEG][SSM_CH];                   // d, d u; then dx, sum_n w A of the tokens walked
-  float dy[Cfg::SEG][SSM_CH];                   // dy; then C . h
-  float b[Cfg::SEG * 4 * NS], c[Cfg::SEG * 4 * NS];
+  alignas(16) float2 d[Cfg::SEG][SSM_CH];       // d, d u; then dx, sum_n w A of the tokens walked
+  alignas(16) float dy[Cfg::SEG][SSM_CH];       // dy; then C . h
+  alignas(16) float b[Cfg::SEG * 4 * NS];
+  alignas(16) float c[Cfg::SEG * 4 * NS];
   float ck[Cfg::GROUPS][NS][SSM_THREADS];       // state before each group
   float red[SSM_THREADS / 32][Cfg::GT][8 * NS]; // a group's dB, dC, one sum per warp
   float cs[2][SSM_THREADS / (SSM_CH / (16 / int(sizeof(T))))][SSM_CH];  // dDskip, ddt_bias

@@ -571,60 +571,59 @@ class Stream:
             pass
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+_raw_stream = torch._C._cuda_getCurrentRawStream   # (device index) -> cudaStream_t
 
 
-def _want(t, name, dtype, shape, like):
-    """t must be a contiguous CUDA tensor of this dtype and shape on like's device."""
+def _want(t, name, dtype, shape, dev):
+    """Address of t, a contiguous tensor of this dtype and shape on CUDA device dev; None for None."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     _need(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
 
 
-def _io(t, name):
-    """dtype code of an operator's main tensor."""
-    _need(t, name)
-    if t.dtype not in _DT:
+def _io(t, name, dim):
+    """(dtype, code, device index, address) of an operator's main tensor."""
+    code = _DT.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be bf16 or fp32")
-    return _DT[t.dtype]
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.dtype, code, t.get_device(), t.data_ptr()
 
 
-class _on:
-    """The device and stream of one call: the tensors' device, and its current stream or the one
-    given. Memory allocated inside belongs to that stream (scratch may be reused as soon as the
-    call's work on it is done), and tensors of other streams that the call reads are recorded on it."""
-
-    def __init__(self, t, stream, reads=()):
-        self.dev, self.given, self.reads, self.old = t.device, stream, reads, None
-
-    def __enter__(self):
-        if self.given is None:
-            self.ctx = None if torch.cuda.current_device() == self.dev.index else \
-                torch.cuda.device(self.dev)
-            if self.ctx is not None:
-                self.ctx.__enter__()
-            return _vp(torch.cuda.current_stream(self.dev).cuda_stream)
-        if self.given.device != self.dev:
-            raise ValueError(f"stream belongs to {self.given.device}, the tensors to {self.dev}")
+def _launch(dev, stream, body, reads):
+    """body(cudaStream_t) on the tensors' device, on its current stream or the one given. What body
+    allocates belongs to that stream (scratch may be reused as soon as the call's work on it is
+    done), and tensors of other streams that the call uses are recorded on it."""
+    if stream is None:
+        if torch.cuda.current_device() == dev:
+            return body(_raw_stream(dev))
+        with torch.cuda.device(dev):
+            return body(_raw_stream(dev))
+    if stream.device.index != dev:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    with torch.cuda.stream(stream):
         if not torch.cuda.is_current_stream_capturing():
-            for t in self.reads:
+            for t in reads:
                 if t is not None:
-                    t.record_stream(self.given)
-        self.ctx = torch.cuda.stream(self.given)
-        self.ctx.__enter__()
-        return _vp(self.given.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+                    t.record_stream(stream)
+        return body(stream.cuda_stream)
 
 
 def _scratch(n, like):
     return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
+
+
+def _fresh(t, lens):
+    """An output like t: rows past a sequence's end, which no kernel writes, are zero."""
+    return torch.empty_like(t) if lens is None else torch.zeros_like(t)
 
 
 def rope_freqs(dims, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -645,56 +644,52 @@ def rope_freqs(dims, *, base: float = 10000.0, scaling: str | None = None, facto
 
 
 def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, stream):
-    dt = _io(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, H, d]")
-    B, N, Hq, d = q.shape
+    ty, dt, dev, _ = _io(q, "q", 4)
+    B, N, _, d = q.shape
     dims = (dims,) if isinstance(dims, int) else tuple(dims)
-    if not 1 <= len(dims) <= 4:
+    A = len(dims)
+    if not 1 <= A <= 4:
         raise ValueError("1 to 4 axes")
     if layout not in ("half", "interleaved"):
         raise ValueError('layout must be "half" or "interleaved"')
-    _want(freqs, "freqs", torch.float64, (sum(dims) // 2,), q)
-    per_seq = 0
+    f = _want(freqs, "freqs", torch.float64, (sum(dims) // 2,), dev)
+    per_seq, at = 0, None
     if pos is not None:
-        _need(pos, "pos", torch.int64)
-        if pos.device != q.device:
-            raise ValueError(f"pos is on {pos.device}, expected {q.device}")
-        A, shape = len(dims), tuple(pos.shape)
+        shape = pos.shape
         if shape == (B, N, A) or (A == 1 and shape == (B, N)):
             per_seq = 1
         elif not (shape == (N, A) or (A == 1 and shape == (N,))):
             raise ValueError(f"pos must be [N, axes] or [B, N, axes] (one axis: [N] or [B, N]), got "
-                             f"{shape}")
-    if k is not None:
-        _need(k, "k", q.dtype)
-        if k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != d:
-            raise ValueError("k must have q's batch, tokens and head dim")
-        if k.device != q.device:
-            raise ValueError(f"k is on {k.device}, expected {q.device}")
+                             f"{tuple(shape)}")
+        at = _want(pos, "pos", torch.int64, shape, dev)
     xs = (q,) if k is None else (q, k)
-    ranges = []
-    for x in xs:
-        h0, h1 = (0, x.shape[2]) if heads is None else heads
-        if not 0 <= h0 < h1 <= x.shape[2]:
-            raise ValueError(f"heads {heads} outside 0..{x.shape[2]}")
-        ranges.append((h0, h1))
+    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != d):
+        raise ValueError("k must have q's batch, tokens and head dim")
     if out is not None:
         out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(out) != len(xs):
             raise ValueError("out must have one tensor for each input")
-        for o, x in zip(out, xs):
-            _want(o, "out", x.dtype, x.shape, x)
-    cfg = Rope(len(dims), (ctypes.c_int * 4)(*dims), begin, int(layout == "interleaved"), mscale,
-               _at(pos), per_seq, pos0, _at(freqs))
-    with _on(q, stream, (q, k, freqs, pos) + (out or ())) as st:
-        o = out if out is not None else tuple(torch.empty_like(x) for x in xs)
-        ptr = [v for x, y, (h0, _) in zip(xs, o, ranges) for v in (_ptr(x, h0 * d), _ptr(y, h0 * d))]
-        ptr += [None] * (4 - len(ptr))
-        hs = [v for x, (h0, h1) in zip(xs, ranges) for v in (h1 - h0, x.shape[2])]
-        hs += [0] * (4 - len(hs))
+    cfg = Rope(A, (ctypes.c_int * 4)(*dims), begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
+
+    def body(st):
+        ptr, hs, os = [], [], []
+        for i, x in enumerate(xs):
+            H = x.shape[2]
+            h0, h1 = (0, H) if heads is None else heads
+            if not 0 <= h0 < h1 <= H:
+                raise ValueError(f"heads {heads} outside 0..{H}")
+            o = torch.empty_like(x) if out is None else out[i]
+            off = h0 * d * x.element_size()
+            ptr += (_want(x, "qk"[i], ty, x.shape, dev) + off, _want(o, "out", ty, x.shape, dev) + off)
+            hs += (h1 - h0, H)
+            os.append(o)
+        if k is None:
+            ptr += (None, None)
+            hs += (0, 0)
         _check(fn(ctypes.byref(cfg), *ptr, Shape(B, 1, N, d, dt), *hs, st), fn.__name__)
-    return o[0] if k is None else o
+        return os[0] if k is None else tuple(os)
+
+    return _launch(dev, stream, body, xs + (freqs, pos) + (out or ()))
 
 
 def rope_fwd(q, k=None, *, freqs, dims, begin: int = 0, layout: str = "half", mscale: float = 1.0,
@@ -717,22 +712,16 @@ def rope_bwd(dq, dk=None, *, freqs, dims, begin: int = 0, layout: str = "half", 
 
 
 def _conv_args(x, w, bias, silu, S0, lens, step=False):
-    dt = _io(x, "x")
-    if x.dim() != (2 if step else 3):
-        raise ValueError("x must be [B, D]" if step else "x must be [B, L, D]")
+    ty, dt, dev, at = _io(x, "x", 2 if step else 3)
     B, D = x.shape[0], x.shape[-1]
-    L = 1 if step else x.shape[1]
     if w.dim() != 2:
         raise ValueError("w must be [D, K]")
     K = w.shape[1]
-    _want(w, "w", torch.float32, (D, K), x)
-    if bias is not None:
-        _want(bias, "bias", torch.float32, (D,), x)
-    if S0 is not None:
-        _want(S0, "S0", x.dtype, (B, K - 1, D), x)
-    if lens is not None:
-        _want(lens, "lens", torch.int32, (B,), x)
-    return ShortConv(B, L, D, K, dt, int(silu), _at(x), _at(w), _at(bias), _at(S0), _at(lens))
+    return ShortConv(B, 1 if step else x.shape[1], D, K, dt, bool(silu), at,
+                     _want(w, "w", torch.float32, (D, K), dev),
+                     _want(bias, "bias", torch.float32, (D,), dev),
+                     _want(S0, "S0", ty, (B, K - 1, D), dev),
+                     _want(lens, "lens", torch.int32, (B,), dev)), ty, dev
 
 
 def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
@@ -742,14 +731,16 @@ def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
     before the first (zeros without). lens [B] int32: rows of each sequence; o is left alone past them
     (fresh buffers are zero there) and the end state is taken there. Returns o (and the last K - 1
     rows)."""
-    c = _conv_args(x, w, bias, silu, S0, lens)
-    if out is not None:
-        _want(out, "out", x.dtype, x.shape, x)
-    with _on(x, stream, (x, w, bias, S0, lens, out)) as st:
-        o = out if out is not None else torch.empty_like(x) if lens is None else torch.zeros_like(x)
-        S = torch.empty((c.B, c.K - 1, c.D), device=x.device, dtype=x.dtype) if return_state else None
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _at(o), _at(S), st), "kta_short_conv_fwd")
-    return (o, S) if return_state else o
+    c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
+
+    def body(st):
+        o = _fresh(x, lens) if out is None else out
+        S = torch.empty((c.B, c.K - 1, c.D), device=x.device, dtype=ty) if return_state else None
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _want(o, "out", ty, x.shape, dev),
+                                       None if S is None else S.data_ptr(), st), "kta_short_conv_fwd")
+        return (o, S) if return_state else o
+
+    return _launch(dev, stream, body, (x, w, bias, S0, lens, out))
 
 
 def short_conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None, out=None,
@@ -758,17 +749,16 @@ def short_conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None
     state_out). Returns o [B, D]."""
     if state is None:
         raise ValueError("state must be a tensor")
-    c = _conv_args(x, w, bias, silu, state, None, step=True)
-    if state_out is not None:
-        _want(state_out, "state_out", x.dtype, state.shape, x)
-    if out is not None:
-        _want(out, "out", x.dtype, x.shape, x)
-    with _on(x, stream, (x, w, bias, state, state_out, out)) as st:
+    c, ty, dev = _conv_args(x, w, bias, silu, state, None, step=True)
+    end = c.S0 if state_out is None else _want(state_out, "state_out", ty, state.shape, dev)
+
+    def body(st):
         o = torch.empty_like(x) if out is None else out
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _at(o),
-                                       _at(state if state_out is None else state_out), st),
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _want(o, "out", ty, x.shape, dev), end, st),
                "kta_short_conv_fwd")
-    return o
+        return o
+
+    return _launch(dev, stream, body, (x, w, bias, state, state_out, out))
 
 
 def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=None, dS_out=None,
@@ -776,47 +766,40 @@ def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=No
     """Gradients (dx, dw, dbias, dS0) of sum(dout * o) + sum(dS_out * S_out) of short_conv_fwd; dbias
     and dS0 are None without bias and S0. dx is left alone past a sequence's end (a fresh buffer is
     zero there); out = a buffer for dx."""
-    c = _conv_args(x, w, bias, silu, S0, lens)
-    _want(dout, "dout", x.dtype, x.shape, x)
-    if dS_out is not None:
-        _want(dS_out, "dS_out", x.dtype, (c.B, c.K - 1, c.D), x)
-    if out is not None:
-        _want(out, "out", x.dtype, x.shape, x)
-    with _on(x, stream, (x, w, bias, S0, lens, dout, dS_out, out)) as st:
-        dx = out if out is not None else torch.empty_like(x) if lens is None else torch.zeros_like(x)
+    c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
+    g = _want(dout, "dout", ty, x.shape, dev)
+    e = _want(dS_out, "dS_out", ty, (c.B, c.K - 1, c.D), dev)
+
+    def body(st):
+        dx = _fresh(x, lens) if out is None else out
         dw = torch.empty_like(w)
         dbias = None if bias is None else torch.empty_like(bias)
         dS0 = None if S0 is None else torch.empty_like(S0)
-        ws = _scratch(n := _lib.kta_short_conv_bwd_workspace(ctypes.byref(c)), x)
-        _check(_lib.kta_short_conv_bwd(ctypes.byref(c), _at(dout), _at(dS_out), _at(dx), _at(dw),
-                                       _at(dbias), _at(dS0), _at(ws), n, st), "kta_short_conv_bwd")
-    return dx, dw, dbias, dS0
+        n = _lib.kta_short_conv_bwd_workspace(ctypes.byref(c))
+        ws = _scratch(n, x)
+        _check(_lib.kta_short_conv_bwd(
+            ctypes.byref(c), g, e, _want(dx, "out", ty, x.shape, dev), dw.data_ptr(),
+            None if dbias is None else dbias.data_ptr(), None if dS0 is None else dS0.data_ptr(),
+            None if ws is None else ws.data_ptr(), n, st), "kta_short_conv_bwd")
+        return dx, dw, dbias, dS0
+
+    return _launch(dev, stream, body, (x, w, bias, S0, lens, dout, dS_out, out))
 
 
 def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, step=False):
-    ty = _io(u, "u")
-    if u.dim() != (2 if step else 3):
-        raise ValueError("u must be [B, D]" if step else "u must be [B, L, D]")
+    ty, code, dev, at = _io(u, "u", 2 if step else 3)
     if A.dim() != 2 or Bm.dim() != u.dim() + 1:
         raise ValueError("A must be [D, N], Bm and Cm [B, G, N]" if step else
                          "A must be [D, N], Bm and Cm [B, L, G, N]")
-    Bn, C, N, G = u.shape[0], u.shape[-1], A.shape[1], Bm.shape[-2]
-    _want(dt, "dt", u.dtype, u.shape, u)
-    _want(A, "A", torch.float32, (C, N), u)
-    _want(Bm, "Bm", u.dtype, u.shape[:-1] + (G, N), u)
-    _want(Cm, "Cm", u.dtype, Bm.shape, u)
-    if D is not None:
-        _want(D, "D", torch.float32, (C,), u)
-    if z is not None:
-        _want(z, "z", u.dtype, u.shape, u)
-    if dt_bias is not None:
-        _want(dt_bias, "dt_bias", torch.float32, (C,), u)
-    if S0 is not None:
-        _want(S0, "S0", torch.float32, (Bn, C, N), u)
-    if lens is not None:
-        _want(lens, "lens", torch.int32, (Bn,), u)
-    return Ssm(Bn, 1 if step else u.shape[1], C, N, G, ty, _at(u), _at(dt), _at(A), _at(Bm), _at(Cm),
-               _at(D), _at(z), _at(dt_bias), _at(S0), _at(lens))
+    shape, f32 = u.shape, torch.float32
+    B, C, N, G = shape[0], shape[-1], A.shape[1], Bm.shape[-2]
+    bc = shape[:-1] + (G, N)
+    return Ssm(B, 1 if step else shape[1], C, N, G, code, at, _want(dt, "dt", ty, shape, dev),
+               _want(A, "A", f32, (C, N), dev), _want(Bm, "Bm", ty, bc, dev),
+               _want(Cm, "Cm", ty, bc, dev), _want(D, "D", f32, (C,), dev),
+               _want(z, "z", ty, shape, dev), _want(dt_bias, "dt_bias", f32, (C,), dev),
+               _want(S0, "S0", f32, (B, C, N), dev), _want(lens, "lens", torch.int32, (B,), dev)), \
+        ty, dev
 
 
 def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
@@ -826,16 +809,19 @@ def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, len
     [B, L, G, N] like u, group g for channels g D/G ..; D, dt_bias [D] fp32; S0 [B, D, N] fp32. lens
     [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
     end state is taken there. Returns y (and the end state)."""
-    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
-    if out is not None:
-        _want(out, "out", u.dtype, u.shape, u)
-    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, out)) as st:
-        y = out if out is not None else torch.empty_like(u) if lens is None else torch.zeros_like(u)
+    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+
+    def body(st):
+        y = _fresh(u, lens) if out is None else out
         S = torch.empty((c.B, c.D, c.N), device=u.device, dtype=torch.float32) if return_state else None
-        ws = _scratch(n := _lib.kta_ssm_scan_fwd_workspace(ctypes.byref(c)), u)
-        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), _at(y), _at(S), _at(ws), n, st),
-               "kta_ssm_scan_fwd")
-    return (y, S) if return_state else y
+        n = _lib.kta_ssm_scan_fwd_workspace(ctypes.byref(c))
+        ws = _scratch(n, u)
+        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), _want(y, "out", ty, u.shape, dev),
+                                     None if S is None else S.data_ptr(),
+                                     None if ws is None else ws.data_ptr(), n, st), "kta_ssm_scan_fwd")
+        return (y, S) if return_state else y
+
+    return _launch(dev, stream, body, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, out))
 
 
 def ssm_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, state_out=None, out=None,
@@ -844,17 +830,16 @@ def ssm_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, stat
     in place (or into state_out). Returns y [B, D]."""
     if state is None:
         raise ValueError("state must be a tensor")
-    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
-    if state_out is not None:
-        _want(state_out, "state_out", torch.float32, state.shape, u)
-    if out is not None:
-        _want(out, "out", u.dtype, u.shape, u)
-    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, state, state_out, out)) as st:
+    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
+    end = c.S0 if state_out is None else _want(state_out, "state_out", torch.float32, state.shape, dev)
+
+    def body(st):
         y = torch.empty_like(u) if out is None else out
-        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), _at(y),
-                                      _at(state if state_out is None else state_out), st),
+        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), _want(y, "out", ty, u.shape, dev), end, st),
                "kta_ssm_scan_step")
-    return y
+        return y
+
+    return _launch(dev, stream, body, (u, dt, A, Bm, Cm, D, z, dt_bias, state, state_out, out))
 
 
 def ssm_scan_bwd(u, dt, A, Bm, Cm, dout, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
@@ -862,29 +847,31 @@ def ssm_scan_bwd(u, dt, A, Bm, Cm, dout, *, D=None, z=None, dt_bias=None, S0=Non
     """Gradients of sum(dout * y) + sum(dS_out * S_out) of ssm_scan_fwd, as a dict: du, ddt, dA, dB,
     dC, and dD, dz, ddt_bias, dS0 (None where the input is). du, ddt, dz, dB, dC are left alone past a
     sequence's end (fresh buffers are zero there); out = a dict of buffers for any of these five."""
-    c = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
-    _want(dout, "dout", u.dtype, u.shape, u)
-    if dS_out is not None:
-        _want(dS_out, "dS_out", torch.float32, (c.B, c.D, c.N), u)
+    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    do = _want(dout, "dout", ty, u.shape, dev)
+    ds = _want(dS_out, "dS_out", torch.float32, (c.B, c.D, c.N), dev)
     out = {k: t for k, t in (out or {}).items() if t is not None}
     like = {"du": u, "ddt": dt, "dz": z, "dB": Bm, "dC": Cm}
     for n, t in out.items():
         if like.get(n) is None:
             raise ValueError(f"no gradient {n!r} to write into out")
-        _want(t, n, u.dtype, like[n].shape, u)
-    with _on(u, stream, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, dout, dS_out,
-                         *out.values())) as st:
-        fresh = torch.empty_like if lens is None else torch.zeros_like
-        g = {n: None if t is None else out[n] if n in out else fresh(t) for n, t in like.items()}
+        _want(t, n, ty, like[n].shape, dev)
+
+    def body(st):
+        g = {n: None if t is None else out[n] if n in out else _fresh(t, lens) for n, t in like.items()}
         for n, t in (("dA", A), ("dD", D), ("ddt_bias", dt_bias), ("dS0", S0)):
             g[n] = None if t is None else torch.empty_like(t)
-        ws = _scratch(n := _lib.kta_ssm_scan_bwd_workspace(ctypes.byref(c)), u)
-        grads = SsmGrads(_at(dout), _at(dS_out), _at(g["du"]), _at(g["ddt"]), _at(g["dA"]),
-                         _at(g["dB"]), _at(g["dC"]), _at(g["dD"]), _at(g["dz"]), _at(g["ddt_bias"]),
-                         _at(g["dS0"]))
-        _check(_lib.kta_ssm_scan_bwd(ctypes.byref(c), ctypes.byref(grads), _at(ws), n, st),
-               "kta_ssm_scan_bwd")
-    return g
+        at = {n: None if t is None else t.data_ptr() for n, t in g.items()}
+        n = _lib.kta_ssm_scan_bwd_workspace(ctypes.byref(c))
+        ws = _scratch(n, u)
+        grads = SsmGrads(do, ds, at["du"], at["ddt"], at["dA"], at["dB"], at["dC"], at["dD"], at["dz"],
+                         at["ddt_bias"], at["dS0"])
+        _check(_lib.kta_ssm_scan_bwd(ctypes.byref(c), ctypes.byref(grads),
+                                     None if ws is None else ws.data_ptr(), n, st), "kta_ssm_scan_bwd")
+        return g
+
+    return _launch(dev, stream, body,
+                   (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, dout, dS_out, *out.values()))
 
 
 def device_status(stream=None):
