@@ -147,14 +147,17 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
   } else {
     p.n_items = s.d / V;
   }
-  // a thread's item serves every head of the block: as many tokens as make one item per thread, and
-  // the heads split over blocks until the card is full
-  p.tt = std::max(1, kta::ROPE_THREADS / p.n_items);
+  // Long inputs: as many tokens as make one item per thread, whose cosines then serve every head of both
+  // tensors. Short ones: fewer tokens and several threads to an item's heads, so that two blocks come to
+  // each SM; when tokens alone are too few for that, the heads are split over blocks too.
+  const long long spread = std::max<long long>(1, rows / (2LL * sm_count()));
+  p.tt = static_cast<int>(std::min<long long>(spread, std::max(1, kta::ROPE_THREADS / p.n_items)));
+  p.lanes = std::max(1, kta::ROPE_THREADS / (p.tt * p.n_items));
   const int Hall = Hs[0] + Hs[1];
   const long long gx = (rows + p.tt - 1) / p.tt;
   if ((r = check_grid(gx))) return r;
-  const long long want = std::max<long long>(1, 4LL * sm_count() / gx);
-  const int step = static_cast<int>(std::max<long long>(1, (Hall + want - 1) / want));
+  const long long want = std::max<long long>(1, 2LL * sm_count() / gx);
+  const int step = static_cast<int>(std::min<long long>(Hall, std::max<long long>(p.lanes, (Hall + want - 1) / want)));
   p.head_step = step;
   const long long gy = (Hall + step - 1) / step;
   if (gy > 65535) return fail(KTA_ERR_UNSUPPORTED, "too many heads");
