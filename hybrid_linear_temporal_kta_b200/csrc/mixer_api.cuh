@@ -184,7 +184,17 @@ kta_status check_conv(const kta_short_conv* c) {
   return KTA_OK;
 }
 
-kta::ConvParams conv_params(const kta_short_conv* c, int V, int run) {
+// Tokens per run: long runs re-read fewer rows of their neighbours, short ones fill the card (768 threads
+// on each SM).
+int conv_run(const kta_short_conv* c) {
+  int run = kta::SC_RUN;
+  while (run > kta::SC_MIN_RUN && static_cast<long long>(c->B) * ((c->L + run - 1) / run) * (c->D / kta::SC_V) <
+                                      768LL * sm_count())
+    run /= 2;
+  return run;
+}
+
+kta::ConvParams conv_params(const kta_short_conv* c) {
   kta::ConvParams p{};
   p.x = c->x;
   p.S0 = c->S0;
@@ -195,32 +205,21 @@ kta::ConvParams conv_params(const kta_short_conv* c, int V, int run) {
   p.L = c->L;
   p.D = c->D;
   p.silu = c->silu;
-  p.run = run;
-  p.runs = (c->L + run - 1) / run;
-  p.nch = c->D / V;
+  p.run = conv_run(c);
+  p.runs = (c->L + p.run - 1) / p.run;
+  p.nch = c->D / kta::SC_V;
   return p;
 }
 
-// Tokens per run: long runs re-read fewer rows of their neighbours, short ones fill the card.
-int conv_run(const kta_short_conv* c, int V, int most) {
-  int run = most;
-  while (run > kta::SC_UNROLL &&
-         static_cast<long long>(c->B) * ((c->L + run - 1) / run) * (c->D / V) < 1024LL * sm_count())
-    run /= 2;
-  return run;
-}
-
-constexpr int kConvFwdRun = 32, kConvBwdRun = 32;
-
-long long conv_bwd_blocks(const kta_short_conv* c, int run) {   // (sequence, block of runs)
-  const int runs = (c->L + run - 1) / run;
-  return static_cast<long long>(c->B) * ((runs + kta::SC_BWD_Y - 1) / kta::SC_BWD_Y);
+long long conv_bwd_blocks(const kta::ConvParams& p) {   // (sequence, block of runs)
+  return static_cast<long long>(p.B) * ((p.runs + kta::SC_BWD_Y - 1) / kta::SC_BWD_Y);
 }
 
 template <typename T, int K>
 kta_status launch_conv_fwd(const kta::ConvParams& p, long long blocks, cudaStream_t st) {
   TraceScope ts("short_conv_fwd", st);
-  kta::short_conv_fwd_kernel<T, K><<<static_cast<unsigned>(blocks), kta::SC_THREADS, 0, st>>>(p);
+  const auto kern = p.silu ? kta::short_conv_fwd_kernel<T, K, true> : kta::short_conv_fwd_kernel<T, K, false>;
+  kern<<<static_cast<unsigned>(blocks), kta::SC_THREADS, 0, st>>>(p);
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }
@@ -230,8 +229,8 @@ kta_status launch_conv_bwd(const kta::ConvParams& p, long long blocks, long long
                            float* dbias, cudaStream_t st) {
   {
     TraceScope ts("short_conv_bwd", st);
-    kta::short_conv_bwd_kernel<T, K>
-        <<<static_cast<unsigned>(blocks), kta::SC_BWD_X * kta::SC_BWD_Y, 0, st>>>(p);
+    const auto kern = p.silu ? kta::short_conv_bwd_kernel<T, K, true> : kta::short_conv_bwd_kernel<T, K, false>;
+    kern<<<static_cast<unsigned>(blocks), kta::SC_BWD_X * kta::SC_BWD_Y, 0, st>>>(p);
     KTA_CUDA(cudaGetLastError());
   }
   TraceScope ts("short_conv_dw", st);
@@ -256,8 +255,7 @@ kta_status conv_fwd_common(const kta_short_conv* c, void* o, void* S_out, void* 
                     {o, n, true, true, "o"},
                     {S_out, ns, true, false, "S_out"}};
   if ((r = check_spans(v, 6))) return r;
-  const int V = static_cast<int>(16 / es);
-  kta::ConvParams p = conv_params(c, V, conv_run(c, V, kConvFwdRun));
+  kta::ConvParams p = conv_params(c);
   p.o = o;
   p.S_out = S_out;
   const long long blocks =
@@ -558,8 +556,7 @@ kta_status kta_short_conv_fwd(const kta_short_conv* c, void* o, void* S_out, voi
 
 size_t kta_short_conv_bwd_workspace(const kta_short_conv* c) {
   if (check_conv(c)) return 0;
-  const int run = conv_run(c, 4, kConvBwdRun);
-  return mixer_round(static_cast<size_t>(conv_bwd_blocks(c, run)) * (c->K + 1) * c->D * 4);
+  return mixer_round(static_cast<size_t>(conv_bwd_blocks(conv_params(c))) * (c->K + 1) * c->D * 4);
 }
 
 kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const void* dS_out, void* dx,
@@ -581,13 +578,13 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
                     {dbias, nb, true, false, "dbias"}, {dS0, ns, true, false, "dS0"},
                     {ws, need, true, false, "the workspace"}};
   if ((r = check_spans(v, 11))) return r;
-  kta::ConvParams p = conv_params(c, 4, conv_run(c, 4, kConvBwdRun));
+  kta::ConvParams p = conv_params(c);
   p.dout = dout;
   p.dS_out = dS_out;
   p.dx = dx;
   p.dS0 = dS0;
   p.part = static_cast<float*>(ws);
-  const long long rows = conv_bwd_blocks(c, p.run);
+  const long long rows = conv_bwd_blocks(p);
   const long long blocks = rows * ((p.nch + kta::SC_BWD_X - 1) / kta::SC_BWD_X);
   if ((r = check_grid(blocks))) return r;
   cudaStream_t st = as_stream(stream);
