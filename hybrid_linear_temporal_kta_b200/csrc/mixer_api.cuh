@@ -401,20 +401,23 @@ kta_status launch_ssm_step(const kta::SsmParams& p, cudaStream_t st) {
   return KTA_OK;
 }
 
-template <int NS> int ssm_bwd_seg() { return kta::SsmBwdCfg<NS>::SEG; }
-
-void ssm_bwd_plan(kta::SsmParams& p) {
-  const int ns = ssm_ns(p.N);
-  p.seg = ns == 1 ? ssm_bwd_seg<1>() : ns == 2 ? ssm_bwd_seg<2>() : ns == 4 ? ssm_bwd_seg<4>() : ssm_bwd_seg<8>();
-  p.nseg = (p.L + p.seg - 1) / p.seg;
+void ssm_bwd_plan(kta::SsmBwdParams& p) {
+  p.f.seg = kta::SSM_BWD_SEG;
+  p.f.nseg = (p.f.L + p.f.seg - 1) / p.f.seg;
+  const int np = ssm_np(p.f.N);
+  const int ch = np == 4   ? kta::SsmBwdCfg<4>::BCH
+                 : np == 8 ? kta::SsmBwdCfg<8>::BCH
+                 : np == 16 ? kta::SsmBwdCfg<16>::BCH
+                            : kta::SsmBwdCfg<32>::BCH;
+  p.cbg = (p.f.Dg + ch - 1) / ch;
 }
 
 struct SsmBwdWs {
   size_t h, g, d, c, bc, total;
 };
 
-SsmBwdWs ssm_bwd_ws(const kta::SsmParams& p) {
-  const size_t segs = static_cast<size_t>(p.B) * p.nseg * p.D;
+SsmBwdWs ssm_bwd_ws(const kta::SsmBwdParams& p) {
+  const size_t segs = static_cast<size_t>(p.f.B) * p.f.nseg * p.f.D;
   SsmBwdWs w;
   size_t at = 0;
   auto put = [&](size_t n) {
@@ -422,38 +425,43 @@ SsmBwdWs ssm_bwd_ws(const kta::SsmParams& p) {
     at += mixer_round(n * 4);
     return o;
   };
-  w.h = put(segs * p.N);
-  w.g = put(segs * p.N);
+  w.h = put(segs * ssm_np(p.f.N));
+  w.g = put(segs * ssm_np(p.f.N));
   w.d = put(segs);
   w.c = put(segs * 2);
-  w.bc = put(static_cast<size_t>(p.G) * p.cbg * p.B * p.L * 2 * p.N);
+  w.bc = put(static_cast<size_t>(p.f.G) * p.cbg * p.f.B * p.f.L * 2 * p.f.N);
   w.total = at;
   return w;
 }
 
-template <typename T, int NS>
+template <typename T, int NP>
 kta_status launch_ssm_bwd(const kta::SsmBwdParams& p, cudaStream_t st) {
-  const long long blocks = static_cast<long long>(p.f.B) * p.f.G * p.f.cbg * p.f.nseg;
-  const long long states = static_cast<long long>(p.f.B) * p.f.D * p.f.N;
+  constexpr int W = kta::SSM_THREADS / 32;
+  const long long segs = static_cast<long long>(p.f.B) * p.f.nseg * p.f.G;
+  const long long blocks_l = (segs * p.f.cbg + W - 1) / W, blocks_m = segs * p.cbg;
+  const long long states = static_cast<long long>(p.f.B) * p.f.D * NP;
   const long long bc = static_cast<long long>(p.f.B) * p.f.L * p.f.G * 2 * p.f.N;
   kta_status r;
-  if ((r = check_grid(blocks)) || (r = check_grid((states + 255) / 256)) || (r = check_grid((bc + 255) / 256)))
+  if ((r = check_grid(blocks_l)) || (r = check_grid(blocks_m)) || (r = check_grid((states + 255) / 256)) ||
+      (r = check_grid((bc + 255) / 256)))
     return r;
-  const size_t smem = sizeof(kta::SsmBwdSmem<T, NS>);
-  if ((r = set_smem_attr(kta::ssm_bwd_main_kernel<T, NS>, smem))) return r;
+  const size_t smem_l = W * sizeof(kta::SsmLocalSmem<T, NP>), smem_m = sizeof(kta::SsmMainSmem<T, NP>);
+  if ((r = set_smem_attr(kta::ssm_bwd_local_kernel<T, NP>, smem_l)) ||
+      (r = set_smem_attr(kta::ssm_bwd_main_kernel<T, NP>, smem_m)))
+    return r;
   {
     TraceScope ts("ssm_bwd_local", st);
-    kta::ssm_bwd_local_kernel<T, NS><<<static_cast<unsigned>(blocks), kta::SSM_THREADS, 0, st>>>(p);
+    kta::ssm_bwd_local_kernel<T, NP><<<static_cast<unsigned>(blocks_l), kta::SSM_THREADS, smem_l, st>>>(p);
     KTA_CUDA(cudaGetLastError());
   }
   {
     TraceScope ts("ssm_bwd_carry", st);
-    kta::ssm_bwd_carry_kernel<<<static_cast<unsigned>((states + 255) / 256), 256, 0, st>>>(p);
+    kta::ssm_bwd_carry_kernel<<<dim3(static_cast<unsigned>((states + 255) / 256), 2), 256, 0, st>>>(p, NP);
     KTA_CUDA(cudaGetLastError());
   }
   {
     TraceScope ts("ssm_bwd_main", st);
-    kta::ssm_bwd_main_kernel<T, NS><<<static_cast<unsigned>(blocks), kta::SSM_THREADS, smem, st>>>(p);
+    kta::ssm_bwd_main_kernel<T, NP><<<static_cast<unsigned>(blocks_m), kta::SSM_THREADS, smem_m, st>>>(p);
     KTA_CUDA(cudaGetLastError());
   }
   {
@@ -464,7 +472,7 @@ kta_status launch_ssm_bwd(const kta::SsmBwdParams& p, cudaStream_t st) {
   TraceScope ts("ssm_bwd_param", st);
   const long long nA = static_cast<long long>(p.f.D) * p.f.N;
   const long long pb = (nA + 31) / 32 + (2LL * p.f.D + 31) / 32;
-  kta::ssm_bwd_param_kernel<<<static_cast<unsigned>(pb), 256, 0, st>>>(p);
+  kta::ssm_bwd_param_kernel<<<static_cast<unsigned>(pb), 256, 0, st>>>(p, NP);
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }
@@ -651,7 +659,8 @@ kta_status kta_ssm_scan_step(const kta_ssm* c, void* y, float* S_out, void* stre
 
 size_t kta_ssm_scan_bwd_workspace(const kta_ssm* c) {
   if (check_ssm(c)) return 0;
-  kta::SsmParams p = ssm_params(c);
+  kta::SsmBwdParams p{};
+  p.f = ssm_params(c);
   ssm_bwd_plan(p);
   return ssm_bwd_ws(p).total;
 }
@@ -665,8 +674,8 @@ kta_status kta_ssm_scan_bwd(const kta_ssm* c, const kta_ssm_grads* g, void* ws, 
   if (g->dD_skip && !c->D_skip) return fail(KTA_ERR_INVALID_ARG, "dD_skip without D_skip");
   kta::SsmBwdParams p{};
   p.f = ssm_params(c);
-  ssm_bwd_plan(p.f);
-  const SsmBwdWs w = ssm_bwd_ws(p.f);
+  ssm_bwd_plan(p);
+  const SsmBwdWs w = ssm_bwd_ws(p);
   if ((r = check_ws(ws, ws_bytes, w.total))) return r;
   Span v[kSsmInputs + 12];
   ssm_inputs(c, v);
@@ -703,7 +712,7 @@ kta_status kta_ssm_scan_bwd(const kta_ssm* c, const kta_ssm_grads* g, void* ws, 
   p.part_c = reinterpret_cast<float*>(base + w.c);
   p.part_bc = reinterpret_cast<float*>(base + w.bc);
   cudaStream_t st = as_stream(stream);
-  KTA_SSM_DISPATCH(launch_ssm_bwd, c->dtype, c->N, p, st);
+  KTA_SSM_FWD_DISPATCH(launch_ssm_bwd, c->dtype, c->N, p, st);
 }
 
 }  // extern "C"

@@ -32,17 +32,18 @@ struct SsmBlock {
   int b, s, g, c0, cw;           // sequence, segment, group, first channel, channels
 };
 
-__device__ __forceinline__ SsmBlock ssm_block(const SsmParams& p, long long blk, int nseg) {
+// Warp `wid` of a grid over (sequence, segment, group, channel block of CH).
+__device__ __forceinline__ SsmBlock ssm_block(const SsmParams& p, long long wid, int nseg, int cbg, int CH) {
   SsmBlock k;
-  const int ncb = p.G * p.cbg;
-  const long long rest = blk / ncb;
-  const int cb = static_cast<int>(blk - rest * ncb);
+  const int ncb = p.G * cbg;
+  const long long rest = wid / ncb;
+  const int cb = static_cast<int>(wid - rest * ncb);
   k.b = static_cast<int>(rest / nseg);
   k.s = static_cast<int>(rest - static_cast<long long>(k.b) * nseg);
-  k.g = cb / p.cbg;
-  const int o = (cb - k.g * p.cbg) * SSM_CH;
+  k.g = cb / cbg;
+  const int o = (cb - k.g * cbg) * CH;
   k.c0 = k.g * p.Dg + o;
-  k.cw = min(SSM_CH, p.Dg - o);
+  k.cw = min(CH, p.Dg - o);
   return k;
 }
 
@@ -73,41 +74,66 @@ __device__ __forceinline__ void ssm_store_states(float* row, int q, int N, const
   }
 }
 
-template <int NS>
-__device__ __forceinline__ void lds_states(const float* s, float (&f)[NS]) {
-  if constexpr (NS % 4 == 0) {
+// Starts the copies of TT rows of B (and of C, if C) to their raw tile.
+template <typename T, int NP, int TT, bool C, int BYTES>
+__device__ __forceinline__ void ssm_rows_fetch_as(const SsmParams& p, T (*rb)[NP], T (*rc)[NP], long long row0, int g,
+                                                  int t0, int t_end, int lane) {
+  constexpr int V = BYTES / int(sizeof(T)) > 0 ? BYTES / int(sizeof(T)) : 1, NV = (NP + V - 1) / V;
 #pragma unroll
-    for (int i = 0; i < NS / 4; ++i)
-      *reinterpret_cast<float4*>(f + 4 * i) = reinterpret_cast<const float4*>(s)[i];
-  } else if constexpr (NS == 2) {
-    *reinterpret_cast<float2*>(f) = *reinterpret_cast<const float2*>(s);
-  } else {
-    f[0] = s[0];
+  for (int m = 0; m < (TT * NV + 31) / 32; ++m) {
+    const int it = lane + m * 32, t = it / NV, n = it % NV * V;
+    if (it < TT * NV && n < p.N) {
+      const bool on = t0 + t < t_end;
+      const long long at = on ? ((row0 + t0 + t) * p.G + g) * p.N + n : 0;
+      piece_async<BYTES>(&rb[t][n], static_cast<const T*>(p.Bm) + at, on);
+      if (C) piece_async<BYTES>(&rc[t][n], static_cast<const T*>(p.Cm) + at, on);
+    }
   }
 }
+template <typename T, int NP, int TT, bool C>
+__device__ __forceinline__ void ssm_rows_fetch(const SsmParams& p, T (*rb)[NP], T (*rc)[NP], long long row0, int g,
+                                               int t0, int t_end, int lane) {
+  if (p.bc_bytes == 16)
+    ssm_rows_fetch_as<T, NP, TT, C, 16>(p, rb, rc, row0, g, t0, t_end, lane);
+  else if (p.bc_bytes == 8)
+    ssm_rows_fetch_as<T, NP, TT, C, 8>(p, rb, rc, row0, g, t0, t_end, lane);
+  else if (p.bc_bytes == 4)
+    ssm_rows_fetch_as<T, NP, TT, C, 4>(p, rb, rc, row0, g, t0, t_end, lane);
+}
 
-// Copies rows t0 .. t0 + TT - 1 of B (or C), group g, to fp32 rows of 4 NS; rows from `end` on are 0.
-template <typename T, int NS, int TT>
-__device__ __forceinline__ void ssm_stage_bc(const SsmParams& p, const void* src, int b, int g, int t0,
-                                             int end, float* dst) {
-  constexpr int V = 16 / int(sizeof(T));
-  const T* rows = static_cast<const T*>(src);
-  const long long ld = static_cast<long long>(p.G) * p.N;
-  const long long r0 = (static_cast<long long>(b) * p.L + t0) * ld + g * p.N;
-  if (p.bc_bytes == 16) {
-    const int nv = p.N / V;
-    for (int i = threadIdx.x; i < TT * nv; i += SSM_THREADS) {
-      const int t = i / nv, v = i - t * nv;
-      VecPack<T, V> x;
-      x.zero();
-      if (t0 + t < end) x.load(rows + r0 + t * ld + v * V);
+// The raw rows (or, for odd rows of 2-byte elements, rows from memory) as fp32; columns from N on are
+// left as they are (zeros, set once).
+template <typename T, int NP, int TT, bool C>
+__device__ __forceinline__ void ssm_rows_f32(const SsmParams& p, const T (*rb)[NP], const T (*rc)[NP],
+                                             float (*bc)[C ? 2 : 1][NP], long long row0, int g, int t0, int t_end,
+                                             int lane) {
+  if (p.bc_bytes) {
+    constexpr int NQ = NP / 4;
 #pragma unroll
-      for (int k = 0; k < V; ++k) dst[t * 4 * NS + v * V + k] = to_f32(x.e[k]);
+    for (int m = 0; m < (TT * NQ + 31) / 32; ++m) {
+      const int it = lane + m * 32, t = it / NQ, n = it % NQ * 4;
+      if (it < TT * NQ && n < p.N) {
+#pragma unroll
+        for (int w = 0; w < (C ? 2 : 1); ++w) {
+          VecPack<T, 4> x;
+          x.load(w ? &rc[t][n] : &rb[t][n]);
+          float4 f = make_float4(to_f32(x.e[0]), to_f32(x.e[1]), to_f32(x.e[2]), to_f32(x.e[3]));
+          if (n + 4 > p.N) {                             // the row ends inside the quad
+            f.y = n + 1 < p.N ? f.y : 0.f;
+            f.z = n + 2 < p.N ? f.z : 0.f;
+            f.w = 0.f;
+          }
+          *reinterpret_cast<float4*>(&bc[t][w][n]) = f;
+        }
+      }
     }
   } else {
-    for (int i = threadIdx.x; i < TT * p.N; i += SSM_THREADS) {
-      const int t = i / p.N, n = i - t * p.N;
-      dst[t * 4 * NS + n] = t0 + t < end ? to_f32(rows[r0 + t * ld + n]) : 0.f;
+    for (int it = lane; it < TT * p.N; it += 32) {
+      const int t = it / p.N, n = it - t * p.N;
+      const bool on = t0 + t < t_end;
+      const long long at = on ? ((row0 + t0 + t) * p.G + g) * p.N + n : 0;
+      bc[t][0][n] = on ? to_f32(static_cast<const T*>(p.Bm)[at]) : 0.f;
+      if (C) bc[t][C ? 1 : 0][n] = on ? to_f32(static_cast<const T*>(p.Cm)[at]) : 0.f;
     }
   }
 }
@@ -142,23 +168,6 @@ static_assert(sizeof(SsmFwdSmem<__nv_bfloat16, 4, false>) % 16 == 0 &&
                   sizeof(SsmFwdSmem<__nv_bfloat16, 4, false>::Raw) % 16 == 0,
               "warps' and stages' parts stay 16-byte aligned");
 
-// One piece size of a tile's rows of B and C.
-template <typename T, int NP, bool OUT, int BYTES, typename Raw>
-__device__ __forceinline__ void ssm_fetch_bc(const SsmParams& p, Raw& r, long long row0, int g, int t0, int t_end,
-                                             int lane) {
-  constexpr int V = BYTES / int(sizeof(T)) > 0 ? BYTES / int(sizeof(T)) : 1, NV = (NP + V - 1) / V;
-#pragma unroll
-  for (int m = 0; m < (SSM_TT * NV + 31) / 32; ++m) {
-    const int it = lane + m * 32, t = it / NV, n = it % NV * V;
-    if (it < SSM_TT * NV && n < p.N) {
-      const bool on = t0 + t < t_end;
-      const long long at = on ? ((row0 + t0 + t) * p.G + g) * p.N + n : 0;
-      piece_async<BYTES>(&r.b[t][n], static_cast<const T*>(p.Bm) + at, on);
-      if (OUT) piece_async<BYTES>(&r.c[t][n], static_cast<const T*>(p.Cm) + at, on);
-    }
-  }
-}
-
 // OUT: outputs (and, past the last segment, the end state) from the state that enters the segment.
 // Otherwise: the segment's end state from zero (seg_h [B][nseg][NP][D]) and its sum of d.
 template <typename T, int NP, bool OUT>
@@ -171,7 +180,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
   const int nseg = OUT ? p.nseg : p.nseg - 1;
   const long long wid = blockIdx.x * static_cast<long long>(SSM_THREADS / 32) + threadIdx.x / 32;
   if (wid >= static_cast<long long>(p.B) * nseg * p.G * p.cbg) return;
-  const SsmBlock k = ssm_block(p, wid, nseg);
+  const SsmBlock k = ssm_block(p, wid, nseg, p.cbg, SSM_CH);
   const bool live = lane < k.cw;
   const int c = k.c0 + (live ? lane : 0);
   const int len = seq_len(p.lens, k.b, p.L);
@@ -189,12 +198,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
       piece_async<16>(&r.d[t][cc], static_cast<const T*>(p.dt) + at, on);
       if (OUT && p.z) piece_async<16>(&r.z[t][cc], static_cast<const T*>(p.z) + at, on);
     }
-    if (p.bc_bytes == 16)
-      ssm_fetch_bc<T, NP, OUT, 16>(p, r, row0, k.g, t0, t_end, lane);
-    else if (p.bc_bytes == 8)
-      ssm_fetch_bc<T, NP, OUT, 8>(p, r, row0, k.g, t0, t_end, lane);
-    else if (p.bc_bytes == 4)
-      ssm_fetch_bc<T, NP, OUT, 4>(p, r, row0, k.g, t0, t_end, lane);
+    ssm_rows_fetch<T, NP, SSM_TT, OUT>(p, r.b, r.c, row0, k.g, t0, t_end, lane);
     piece_commit();
   };
 #pragma unroll
@@ -239,35 +243,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
       if (!OUT) sum_d += d;
       sm.dd[j][lane] = make_float2(d, d * to_f32(r.u[j][lane]));
     }
-    if (p.bc_bytes) {
-      constexpr int NQ = NP / 4;
-#pragma unroll
-      for (int m = 0; m < (SSM_TT * NQ + 31) / 32; ++m) {
-        const int it = lane + m * 32, t = it / NQ, n = it % NQ * 4;
-        if (it < SSM_TT * NQ && n < p.N) {
-#pragma unroll
-          for (int w = 0; w < (OUT ? 2 : 1); ++w) {
-            VecPack<T, 4> x;
-            x.load(w ? &r.c[OUT ? t : 0][n] : &r.b[t][n]);
-            float4 f = make_float4(to_f32(x.e[0]), to_f32(x.e[1]), to_f32(x.e[2]), to_f32(x.e[3]));
-            if (n + 4 > p.N) {                           // the row ends inside the quad
-              f.y = n + 1 < p.N ? f.y : 0.f;
-              f.z = n + 2 < p.N ? f.z : 0.f;
-              f.w = 0.f;
-            }
-            *reinterpret_cast<float4*>(&sm.bc[t][w][n]) = f;
-          }
-        }
-      }
-    } else {                                             // an odd row of 2-byte elements
-      for (int it = lane; it < SSM_TT * p.N; it += 32) {
-        const int t = it / p.N, n = it - t * p.N;
-        const bool on = t0 + t < t_end;
-        const long long at = on ? ((row0 + t0 + t) * p.G + k.g) * p.N + n : 0;
-        sm.bc[t][0][n] = on ? to_f32(static_cast<const T*>(p.Bm)[at]) : 0.f;
-        if (OUT) sm.bc[t][OUT ? 1 : 0][n] = on ? to_f32(static_cast<const T*>(p.Cm)[at]) : 0.f;
-      }
-    }
+    ssm_rows_f32<T, NP, SSM_TT, OUT>(p, r.b, r.c, sm.bc, row0, k.g, t0, t_end, lane);
     __syncwarp();
     fetch(t0 + (STAGES - 1) * SSM_TT, stage == 0 ? STAGES - 1 : stage - 1);   // into the tile before's place
 #pragma unroll
@@ -452,378 +428,554 @@ __global__ __launch_bounds__(SSM_THREADS) void ssm_step_kernel(const SsmParams p
 //     w_t = G_t exp(d_t A) h_{t-1}, dd_t = dx_t u_t + sum_n w_t A, dA = sum_t w_t d_t,
 //     du_t = dx_t d_t + Dskip dy_t, ddt_t = dd_t sigmoid(dt_t + dt_bias),
 //     dz_t = dout_t y_t silu'(z_t), dDskip = sum_t dy_t u_t,       ddt_bias = sum_t ddt_t.
-// Three launches over segments of SEG tokens, all segments at once:
+// Launches over segments of SEG tokens, all segments at once:
 //  1. ssm_bwd_local: each segment's end state from zero, its share of the adjoint that leaves it at
 //     its start (P_t the running product of decays: sum_t P_t dy_t C_t), and its sum of d;
 //  2. ssm_bwd_carry: folds both along the sequence: the state that enters each segment and the
 //     adjoint that enters it from behind (and dS0);
 //  3. ssm_bwd_main: a forward walk keeps the state before every GT tokens in shared memory; then,
-//     last group first, the group's states are formed again in registers and the adjoint walks back.
-// Sums over channels (dB, dC) are joined over a warp by halving exchanges, then over the block, the
-// channel blocks and finally by ssm_bwd_bc in a fixed order; dA, dDskip and ddt_bias likewise.
+//     last group first, the group's states are formed again in registers and the adjoint walks back:
+//     three exponentials per (token, channel, state) in all, and no state but the segments' in memory;
+//  4. ssm_bwd_bc, ssm_bwd_param: sums over channel blocks, and over segments, in a fixed order.
 
-template <int NS> struct SsmBwdCfg {
-  static constexpr int GT = NS <= 4 ? 8 : 4;       // tokens whose states fit in registers
+template <int NP> struct SsmBwdCfg {
+  static constexpr int NH = NP == 32 ? 8 : NP >= 8 ? 4 : 2;   // states of one lane, for each of two channels
+  static constexpr int SPL = NP / NH;                // lanes that share a channel's states (2 or 4)
+  static constexpr int CH = 64 / SPL;                // channels of a warp
+  static constexpr int BCH = CH * SSM_THREADS / 32;  // channels of a block
+  static constexpr int GT = 4;                       // tokens whose decays and states fit in registers
   static constexpr int GROUPS = 8;
   static constexpr int SEG = GT * GROUPS;
+  // sums over the warp's channel pairs: NH values are halved log2(NH) times; where a lane bit is left,
+  // it tells dB from dC
+  static constexpr bool SPLIT = 32 / SPL > NH;
 };
+constexpr int SSM_BWD_SEG = 32;
 
 struct SsmBwdParams {
-  SsmParams f;                   // inputs; nseg / seg of the backward; seg_h: entering states
+  SsmParams f;                   // inputs; nseg / seg of the backward; seg_h [B][nseg][NP][D]
   const void *dout;
   const float* dS_out;
   void *du, *ddt, *dz, *dB, *dC;
   float *dA, *dD, *ddt_bias, *dS0;
-  float* seg_g;                  // [B][nseg][D][N]: adjoint entering each segment from behind
+  int cbg;                       // channel blocks per group of the main pass (f.cbg: of the local one)
+  float* seg_g;                  // [B][nseg][NP][D]: adjoint entering each segment from behind
   float* part_bc;                // [G * cbg][B * L][2 N]
   float* part_c;                 // [B][nseg][2][D]: dDskip, ddt_bias
 };
 
-// (d, d u) and dy of a segment in shared memory; zero past its end.
-template <typename T, int SEG>
-__device__ __forceinline__ void ssm_bwd_stage(const SsmBwdParams& p, const SsmBlock& k, int t0, int t_end,
-                                              float2 (*s_d)[SSM_CH], float (*s_dy)[SSM_CH]) {
-  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V;
-  for (int it = threadIdx.x; it < SEG * CPR; it += SSM_THREADS) {
-    const int t = it / CPR, cc = it % CPR * V;
-    const bool on = t0 + t < t_end && cc < k.cw;
-    VecPack<T, V> u, d, z, o;
-    if (on) {
-      const long long at = (static_cast<long long>(k.b) * p.f.L + t0 + t) * p.f.D + k.c0 + cc;
-      u.load(static_cast<const T*>(p.f.u) + at);
-      d.load(static_cast<const T*>(p.f.dt) + at);
-      o.load(static_cast<const T*>(p.dout) + at);
-      if (p.f.z) z.load(static_cast<const T*>(p.f.z) + at);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float2 v = make_float2(0.f, 0.f);
-      float dy = 0.f;
-      if (on) {
-        v.x = softplus_f32(to_f32(d.e[i]) + (p.f.dt_bias ? p.f.dt_bias[k.c0 + cc + i] : 0.f));
-        v.y = v.x * to_f32(u.e[i]);
-        dy = to_f32(o.e[i]);
-        if (p.f.z) {
-          const float zf = to_f32(z.e[i]);
-          dy *= zf * sigmoid_f32(zf);
-        }
-      }
-      s_d[t][cc + i] = v;
-      s_dy[t][cc + i] = dy;
-    }
-  }
-}
+// Shared memory of one warp of the local pass: as in the forward, with dout and C beside.
+template <typename T, int NP>
+struct SsmLocalSmem {
+  static constexpr int STAGES = 2;
+  struct Raw {
+    alignas(16) T u[SSM_TT][SSM_CH];
+    alignas(16) T d[SSM_TT][SSM_CH];
+    alignas(16) T z[SSM_TT][SSM_CH];
+    alignas(16) T o[SSM_TT][SSM_CH];
+    alignas(16) T b[SSM_TT][NP];
+    alignas(16) T c[SSM_TT][NP];
+  };
+  Raw raw[STAGES];
+  alignas(16) float bc[SSM_TT][2][NP];
+  alignas(16) float2 dd[SSM_TT][SSM_CH];   // d, d u
+  alignas(16) float dy[SSM_TT][SSM_CH];
+};
 
-template <typename T, int NS>
-__global__ __launch_bounds__(SSM_THREADS) void ssm_bwd_local_kernel(const SsmBwdParams p) {
-  using Cfg = SsmBwdCfg<NS>;
-  __shared__ __align__(16) float2 s_d[Cfg::SEG][SSM_CH];
-  __shared__ __align__(16) float s_dy[Cfg::SEG][SSM_CH];
-  __shared__ __align__(16) float s_b[Cfg::SEG * 4 * NS], s_c[Cfg::SEG * 4 * NS];
-  const int tid = threadIdx.x, lane = tid % 32, q = lane % 4;
-  const SsmBlock k = ssm_block(p.f, blockIdx.x, p.f.nseg);
-  const int ch = tid / 32 * 8 + lane / 4;
-  const bool live = ch < k.cw;
-  const long long c = k.c0 + (live ? ch : 0);
+// One warp = 32 channels of a group over one segment, a lane all states of one channel.
+template <typename T, int NP>
+__global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_local_kernel(const SsmBwdParams p) {
+  using Smem = SsmLocalSmem<T, NP>;
+  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, STAGES = Smem::STAGES;
+  extern __shared__ __align__(16) unsigned char ssm_smem[];
+  Smem& sm = reinterpret_cast<Smem*>(ssm_smem)[threadIdx.x / 32];
+  const int lane = threadIdx.x % 32;
+  const long long wid = blockIdx.x * static_cast<long long>(SSM_THREADS / 32) + threadIdx.x / 32;
+  if (wid >= static_cast<long long>(p.f.B) * p.f.nseg * p.f.G * p.f.cbg) return;
+  const SsmBlock k = ssm_block(p.f, wid, p.f.nseg, p.f.cbg, SSM_CH);
+  const bool live = lane < k.cw;
+  const int c = k.c0 + (live ? lane : 0);
   const int len = seq_len(p.f.lens, k.b, p.f.L);
-  const int t0 = k.s * Cfg::SEG, t_end = min(t0 + Cfg::SEG, len);
-  float A2[NS], h[NS], g[NS], P[NS], sum_d = 0.f;
-  ssm_load_states<NS>(p.f.A + c * p.f.N, q, p.f.N, A2);
+  const int t_begin = k.s * p.f.seg, t_end = min(t_begin + p.f.seg, len);
+  const long long row0 = static_cast<long long>(k.b) * p.f.L;
+
+  auto fetch = [&](int t0, int stage) {
+    typename Smem::Raw& r = sm.raw[stage];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    A2[i] *= 1.4426950408889634f;
-    h[i] = g[i] = 0.f;
-    P[i] = 1.f;
+    for (int m = 0; m < SSM_TT * CPR / 32; ++m) {
+      const int it = lane + m * 32, t = it / CPR, cc = it % CPR * V;
+      const bool on = t0 + t < t_end && cc < k.cw;
+      const long long at = on ? (row0 + t0 + t) * p.f.D + k.c0 + cc : 0;
+      piece_async<16>(&r.u[t][cc], static_cast<const T*>(p.f.u) + at, on);
+      piece_async<16>(&r.d[t][cc], static_cast<const T*>(p.f.dt) + at, on);
+      piece_async<16>(&r.o[t][cc], static_cast<const T*>(p.dout) + at, on);
+      if (p.f.z) piece_async<16>(&r.z[t][cc], static_cast<const T*>(p.f.z) + at, on);
+    }
+    ssm_rows_fetch<T, NP, SSM_TT, true>(p.f, r.b, r.c, row0, k.g, t0, t_end, lane);
+    piece_commit();
+  };
+  fetch(t_begin, 0);
+
+  float2 A2[NP / 2], h[NP / 2], g[NP / 2], P[NP / 2];
+  const float* Arow = p.f.A + static_cast<long long>(c) * p.f.N;
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) {
+    A2[i].x = 2 * i < p.f.N ? Arow[2 * i] * 1.4426950408889634f : 0.f;
+    A2[i].y = 2 * i + 1 < p.f.N ? Arow[2 * i + 1] * 1.4426950408889634f : 0.f;
+    h[i] = g[i] = make_float2(0.f, 0.f);
+    P[i] = make_float2(1.f, 1.f);
   }
-  if (t0 < t_end) {
-    for (int i = tid; i < Cfg::SEG * 4 * NS; i += SSM_THREADS) s_b[i] = s_c[i] = 0.f;
-    __syncthreads();
-    ssm_stage_bc<T, NS, Cfg::SEG>(p.f, p.f.Bm, k.b, k.g, t0, t_end, s_b);
-    ssm_stage_bc<T, NS, Cfg::SEG>(p.f, p.f.Cm, k.b, k.g, t0, t_end, s_c);
-    ssm_bwd_stage<T, Cfg::SEG>(p, k, t0, t_end, s_d, s_dy);
-    __syncthreads();
-#pragma unroll 4
-    for (int t = 0; t < Cfg::SEG; ++t) {
-      const float2 d = s_d[t][ch];
-      const float dy = s_dy[t][ch];
-      float bv[NS], cv[NS];
-      lds_states<NS>(s_b + t * 4 * NS + q * NS, bv);
-      lds_states<NS>(s_c + t * 4 * NS + q * NS, cv);
-      sum_d += d.x;
+  for (int i = lane; i < SSM_TT * 2 * NP; i += 32) (&sm.bc[0][0][0])[i] = 0.f;
+  const float bias = p.f.dt_bias ? p.f.dt_bias[c] : 0.f;
+  float sum_d = 0.f;
+  int stage = 0;
+  for (int t0 = t_begin; t0 < t_end; t0 += SSM_TT, stage ^= 1) {
+    piece_wait<0>();
+    __syncwarp();                                        // the pieces are there; dd, dy, bc are free
+    fetch(t0 + SSM_TT, stage ^ 1);
+    typename Smem::Raw& r = sm.raw[stage];
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const float a = ex2_approx(d.x * A2[i]);
-        h[i] = fmaf(a, h[i], d.y * bv[i]);
-        P[i] *= a;
-        g[i] = fmaf(P[i], dy * cv[i], g[i]);
+    for (int j = 0; j < SSM_TT; ++j) {
+      float d = softplus_f32(to_f32(r.d[j][lane]) + bias);
+      d = t0 + j < t_end ? d : 0.f;
+      sum_d += d;
+      float dy = to_f32(r.o[j][lane]);
+      if (p.f.z) {
+        const float z = to_f32(r.z[j][lane]);
+        dy *= z * sigmoid_f32(z);
+      }
+      sm.dd[j][lane] = make_float2(d, d * to_f32(r.u[j][lane]));
+      sm.dy[j][lane] = dy;                               // (past the end 0: dout is)
+    }
+    ssm_rows_f32<T, NP, SSM_TT, true>(p.f, r.b, r.c, sm.bc, row0, k.g, t0, t_end, lane);
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < SSM_TT; ++j) {
+      const float2 dd = sm.dd[j][lane];
+      const float dy = sm.dy[j][lane];
+      const uint64_t d2 = f32x2_pack(dd.x, dd.x), du2 = f32x2_pack(dd.y, dd.y), dy2 = f32x2_pack(dy, dy);
+#pragma unroll
+      for (int i = 0; i < NP / 2; i += 2) {
+        const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(&sm.bc[j][0][2 * i]);
+        const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(&sm.bc[j][1][2 * i]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 x = f32x2_unpack(fmul2(d2, f32x2_pack(A2[i + e])));
+          const uint64_t a = f32x2_pack(ex2_approx(x.x), ex2_approx(x.y));
+          h[i + e] = f32x2_unpack(ffma2(a, f32x2_pack(h[i + e]), fmul2(du2, e ? b4.y : b4.x)));
+          const uint64_t q = fmul2(a, f32x2_pack(P[i + e]));
+          P[i + e] = f32x2_unpack(q);
+          g[i + e] = f32x2_unpack(ffma2(q, fmul2(dy2, e ? c4.y : c4.x), f32x2_pack(g[i + e])));
+        }
       }
     }
   }
   if (!live) return;
-  const long long r = (static_cast<long long>(k.b) * p.f.nseg + k.s) * p.f.D + c;
-  ssm_store_states<NS>(p.f.seg_h + r * p.f.N, q, p.f.N, h);
-  ssm_store_states<NS>(p.seg_g + r * p.f.N, q, p.f.N, g);
-  if (q == 0) p.f.seg_d[r] = sum_d;
+  const long long r = static_cast<long long>(k.b) * p.f.nseg + k.s;
+  float* sh = p.f.seg_h + r * NP * p.f.D + c;
+  float* sg = p.seg_g + r * NP * p.f.D + c;
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) {
+    const long long a = static_cast<long long>(2 * i) * p.f.D, b = a + p.f.D;
+    sh[a] = h[i].x;
+    sh[b] = h[i].y;
+    sg[a] = g[i].x;
+    sg[b] = g[i].y;
+  }
+  p.f.seg_d[r * p.f.D + c] = sum_d;
 }
 
-// One thread per (sequence, channel, state): in place, local end states become entering states and
-// local adjoints become the adjoints entering from behind.
-__global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p) {
-  const long long per = static_cast<long long>(p.f.D) * p.f.N;
+// One thread per (sequence, state, channel), in place: local end states become entering states
+// (blockIdx.y 0), local adjoints the adjoints entering from behind (1).
+__global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p, int NP) {
+  const long long per = static_cast<long long>(p.f.D) * NP;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (gid >= per * p.f.B) return;
   const int b = static_cast<int>(gid / per);
-  const long long e = gid - b * per, c = e / p.f.N;
-  const float A2 = p.f.A[e] * 1.4426950408889634f;
+  const int n = static_cast<int>(gid % per / p.f.D), c = static_cast<int>(gid % p.f.D);
+  const bool on = n < p.f.N, back = blockIdx.y;
+  const long long e = static_cast<long long>(c) * p.f.N + n, eb = static_cast<long long>(b) * p.f.D * p.f.N + e;
+  const float A2 = on ? p.f.A[e] * 1.4426950408889634f : 0.f;
   const int S = p.f.nseg;
-  float* hs = p.f.seg_h + static_cast<long long>(b) * S * per + e;
-  float* gs = p.seg_g + static_cast<long long>(b) * S * per + e;
-  const float* ds = p.f.seg_d + static_cast<long long>(b) * S * p.f.D + c;
-  float h = p.f.S0 ? p.f.S0[b * per + e] : 0.f;
+  const long long first = back ? S - 1 : 0, step = back ? -1 : 1;
+  float* vs = (back ? p.seg_g : p.f.seg_h) + (static_cast<long long>(b) * S + first) * per + gid % per;
+  const float* ds = p.f.seg_d + (static_cast<long long>(b) * S + first) * p.f.D + c;
+  const float* in = back ? p.dS_out : p.f.S0;
+  float h = on && in ? in[eb] : 0.f;
   for (int s0 = 0; s0 < S; s0 += SSM_CARRY_UNROLL) {
     float v[SSM_CARRY_UNROLL], d[SSM_CARRY_UNROLL];
 #pragma unroll
     for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
       if (s0 + i < S) {
-        v[i] = hs[(s0 + i) * per];
-        d[i] = ds[static_cast<long long>(s0 + i) * p.f.D];
+        v[i] = vs[step * (s0 + i) * per];
+        d[i] = ds[step * (s0 + i) * p.f.D];
       }
 #pragma unroll
     for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
       if (s0 + i < S) {
-        hs[(s0 + i) * per] = h;
+        vs[step * (s0 + i) * per] = h;
         h = fmaf(ex2_approx(d[i] * A2), h, v[i]);
       }
   }
-  float g = p.dS_out ? p.dS_out[b * per + e] : 0.f;
-  for (int s0 = S - 1; s0 >= 0; s0 -= SSM_CARRY_UNROLL) {
-    float v[SSM_CARRY_UNROLL], d[SSM_CARRY_UNROLL];
-#pragma unroll
-    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
-      if (s0 - i >= 0) {
-        v[i] = gs[(s0 - i) * per];
-        d[i] = ds[static_cast<long long>(s0 - i) * p.f.D];
-      }
-#pragma unroll
-    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
-      if (s0 - i >= 0) {
-        gs[(s0 - i) * per] = g;
-        g = fmaf(ex2_approx(d[i] * A2), g, v[i]);
-      }
-  }
-  if (p.dS0) p.dS0[b * per + e] = g;
+  if (back && on && p.dS0) p.dS0[eb] = h;
 }
 
-template <typename T, int NS>
-struct SsmBwdSmem {
-  using Cfg = SsmBwdCfg<NS>;
-  alignas(16) float2 d[Cfg::SEG][SSM_CH];       // d, d u; then dx, sum_n w A of the tokens walked
-  alignas(16) float dy[Cfg::SEG][SSM_CH];       // dy; then C . h
-  alignas(16) float b[Cfg::SEG * 4 * NS];
-  alignas(16) float c[Cfg::SEG * 4 * NS];
-  float ck[Cfg::GROUPS][NS][SSM_THREADS];       // state before each group
-  float red[SSM_THREADS / 32][Cfg::GT][8 * NS]; // a group's dB, dC, one sum per warp
-  float cs[2][SSM_THREADS / (SSM_CH / (16 / int(sizeof(T))))][SSM_CH];  // dDskip, ddt_bias
+// Shared memory of a block of the main pass: four warps' own parts, and the rows of B and C.
+template <typename T, int NP>
+struct SsmMainSmem {
+  using Cfg = SsmBwdCfg<NP>;
+  struct Raw {
+    alignas(16) T d[Cfg::SEG][Cfg::CH];
+    alignas(16) T z[Cfg::SEG][Cfg::CH];
+    alignas(16) T o[Cfg::SEG][Cfg::CH];
+  };
+  struct Keep {
+    alignas(16) float4 h[Cfg::GROUPS - 1][Cfg::NH / 2][32];   // state before groups 1 .., by lane
+  };
+  struct Warp {
+    union {                                          // the raw rows are gone before a state is kept
+      Raw raw;
+      Keep ck;
+    };
+    alignas(16) T u[Cfg::SEG][Cfg::CH];
+    alignas(16) float d[Cfg::SEG][Cfg::CH];
+    alignas(16) float dy[Cfg::SEG][Cfg::CH];
+  };
+  Warp w[SSM_THREADS / 32];
+  union {
+    struct {
+      alignas(16) T b[Cfg::SEG][NP];
+      alignas(16) T c[Cfg::SEG][NP];
+    } raw;
+    alignas(16) float red[2][SSM_THREADS / 32][Cfg::GT][2 * NP];   // warps' sums of dB and dC of two groups
+  };
+  alignas(16) float bc[Cfg::SEG][2][NP];
 };
 
-template <typename T, int NS>
-__global__ __launch_bounds__(SSM_THREADS) void ssm_bwd_main_kernel(const SsmBwdParams p) {
-  using Cfg = SsmBwdCfg<NS>;
-  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, GT = Cfg::GT;
-  extern __shared__ __align__(16) unsigned char ssm_smem[];
-  auto& sm = *reinterpret_cast<SsmBwdSmem<T, NS>*>(ssm_smem);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, q = lane % 4;
-  const SsmBlock k = ssm_block(p.f, blockIdx.x, p.f.nseg);
-  const int ch = warp * 8 + lane / 4;
-  const bool live = ch < k.cw;
-  const long long c = k.c0 + (live ? ch : 0);
-  const int len = seq_len(p.f.lens, k.b, p.f.L);
-  const int t0 = k.s * Cfg::SEG, t_end = min(t0 + Cfg::SEG, len);
-  const long long r = (static_cast<long long>(k.b) * p.f.nseg + k.s) * p.f.D + c;
-  const int N = p.f.N;
+__device__ __forceinline__ float2 ssm_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 ssm_pair(const __nv_bfloat16* p) {
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 
-  float dA[NS];
+// H2 packed pairs of neighbouring states.
+template <int H2>
+__device__ __forceinline__ void ssm_lds_pairs(const float* s, uint64_t (&v)[H2]) {
+  if constexpr (H2 % 2 == 0) {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dA[i] = 0.f;
-  if (t0 < t_end) {
-    float A[NS], h[NS], g[NS];
-    ssm_load_states<NS>(p.f.A + c * N, q, N, A);
-    ssm_load_states<NS>(p.f.seg_h + r * N, q, N, h);
-    ssm_load_states<NS>(p.seg_g + r * N, q, N, g);
-    for (int i = tid; i < Cfg::SEG * 4 * NS; i += SSM_THREADS) sm.b[i] = sm.c[i] = 0.f;
-    __syncthreads();
-    ssm_stage_bc<T, NS, Cfg::SEG>(p.f, p.f.Bm, k.b, k.g, t0, t_end, sm.b);
-    ssm_stage_bc<T, NS, Cfg::SEG>(p.f, p.f.Cm, k.b, k.g, t0, t_end, sm.c);
-    ssm_bwd_stage<T, Cfg::SEG>(p, k, t0, t_end, sm.d, sm.dy);
-    __syncthreads();
-    // forward: the state before each group
-#pragma unroll 1
-    for (int gr = 0; gr < Cfg::GROUPS; ++gr) {
+    for (int i = 0; i < H2 / 2; ++i) {
+      const ulonglong2 x = reinterpret_cast<const ulonglong2*>(s)[i];
+      v[2 * i] = x.x;
+      v[2 * i + 1] = x.y;
+    }
+  } else {
+    v[0] = *reinterpret_cast<const unsigned long long*>(s);
+  }
+}
+
+// CNT values summed over the lanes of mask bits [lowest, 16]: halved from mask 16 down while more than
+// one is left, then added. The kept value's index comes back in `at`.
+template <int CNT>
+__device__ __forceinline__ float ssm_sum_lanes(float (&v)[CNT], int lane, int lowest, int& at) {
+  int n = CNT;
+  at = 0;
 #pragma unroll
-      for (int i = 0; i < NS; ++i) sm.ck[gr][i][tid] = h[i];
-      if (gr + 1 < Cfg::GROUPS) {
-#pragma unroll
-        for (int j = 0; j < GT; ++j) {
-          const float2 d = sm.d[gr * GT + j][ch];
-          float bv[NS];
-          lds_states<NS>(sm.b + (gr * GT + j) * 4 * NS + q * NS, bv);
-#pragma unroll
-          for (int i = 0; i < NS; ++i)
-            h[i] = fmaf(ex2_approx(d.x * (A[i] * 1.4426950408889634f)), h[i], d.y * bv[i]);
-        }
+  for (int mask = 16; mask >= 1; mask /= 2) {
+    if (mask >= lowest) {
+      if (n > 1) {
+        halve_sum(v, n, mask, lane & mask);
+        n /= 2;
+        at += lane & mask ? n : 0;
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], mask);
       }
     }
-    // backward, last group first
-#pragma unroll 1
-    for (int gr = Cfg::GROUPS - 1; gr >= 0; --gr) {
-      float a[GT][NS], ah[GT][NS], yv[GT], xv[GT], sv[GT];
+  }
+  return v[0];
+}
+
+// One block = one segment x BCH channels of a group. A lane holds NH states of two neighbouring channels,
+// SPL lanes a channel pair: two channels to a lane halve the exchanges that sum dB and dC over channels,
+// and 2 x NH states x 4 tokens of decays and decayed states stay in registers.
+template <typename T, int NP>
+__global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_kernel(const SsmBwdParams p) {
+  using Cfg = SsmBwdCfg<NP>;
+  using Smem = SsmMainSmem<T, NP>;
+  constexpr int NH = Cfg::NH, H2 = NH / 2, SPL = Cfg::SPL, CH = Cfg::CH, GT = Cfg::GT, SEG = Cfg::SEG,
+                V = 16 / int(sizeof(T)), CPR = CH / V, FT = GT / (SPL / 2);
+  static_assert(SEG == SSM_BWD_SEG, "the plan cuts segments of this length");
+  static_assert(SPL == 2 || SPL == 4, "two or four lanes share a channel pair");
+  extern __shared__ __align__(16) unsigned char ssm_smem[];
+  Smem& sb = *reinterpret_cast<Smem*>(ssm_smem);
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, q = lane % SPL, cp = lane / SPL, N = p.f.N;
+  typename Smem::Warp& sm = sb.w[warp];
+  const SsmBlock k = ssm_block(p.f, blockIdx.x, p.f.nseg, p.cbg, Cfg::BCH);
+  const int wc = warp * CH, lc = 2 * cp;               // the warp's first channel in the block, the lane's in the warp
+  const bool live = wc + lc < k.cw;                    // (a group's last block may leave whole warps idle)
+  const int fc = lc + q % 2;                           // the channel whose rows this lane finishes
+  const int c = k.c0 + (live ? wc + lc : 0), cf = k.c0 + (live ? wc + fc : 0);
+  const int len = seq_len(p.f.lens, k.b, p.f.L);
+  const int t0 = k.s * SEG, t_end = min(t0 + SEG, len);
+  const long long row0 = static_cast<long long>(k.b) * p.f.L;
+  const long long seg = static_cast<long long>(k.b) * p.f.nseg + k.s;
+  float* seg_h = p.f.seg_h + (seg * NP + q * NH) * p.f.D + c;
+  float2 dA[2][H2];                                    // [channel][pair of states]
+  float sD = 0.f, sT = 0.f;
 #pragma unroll
-      for (int i = 0; i < NS; ++i) h[i] = sm.ck[gr][i][tid];
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int i = 0; i < H2; ++i) dA[e][i] = make_float2(0.f, 0.f);
+
+  if (t0 < t_end) {
+    // raw rows of the segment
+#pragma unroll
+    for (int m = 0; m < SEG * CPR / 32; ++m) {
+      const int it = lane + m * 32, t = it / CPR, cc = it % CPR * V;
+      const bool on = t0 + t < t_end && wc + cc < k.cw;
+      const long long at = on ? (row0 + t0 + t) * p.f.D + k.c0 + wc + cc : 0;
+      piece_async<16>(&sm.u[t][cc], static_cast<const T*>(p.f.u) + at, on);
+      piece_async<16>(&sm.raw.d[t][cc], static_cast<const T*>(p.f.dt) + at, on);
+      piece_async<16>(&sm.raw.o[t][cc], static_cast<const T*>(p.dout) + at, on);
+      if (p.f.z) piece_async<16>(&sm.raw.z[t][cc], static_cast<const T*>(p.f.z) + at, on);
+    }
+    if (warp == 0) ssm_rows_fetch<T, NP, SEG, true>(p.f, sb.raw.b, sb.raw.c, row0, k.g, t0, t_end, lane);
+    piece_commit();
+    for (int i = threadIdx.x; i < SEG * 2 * NP; i += SSM_THREADS) (&sb.bc[0][0][0])[i] = 0.f;
+
+    // a lane without a channel works on zeros
+    float2 A[2][H2], g[2][H2], h[2][H2];
+    const float* sg = p.seg_g + (seg * NP + q * NH) * p.f.D + c;
+    auto load_pairs = [&](const float* src, float2 (&v)[2][H2]) {
+#pragma unroll
+      for (int i = 0; i < H2; ++i) {
+        const float2 z2 = make_float2(0.f, 0.f);
+        const float2 a = live ? ssm_pair(src + static_cast<long long>(2 * i) * p.f.D) : z2;
+        const float2 b = live ? ssm_pair(src + static_cast<long long>(2 * i + 1) * p.f.D) : z2;
+        v[0][i] = make_float2(a.x, b.x);
+        v[1][i] = make_float2(a.y, b.y);
+      }
+    };
+    load_pairs(seg_h, h);
+    load_pairs(sg, g);
+#pragma unroll
+    for (int i = 0; i < H2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = q * NH + 2 * i;
+        const float* Arow = p.f.A + static_cast<long long>(c + e) * N;
+        A[e][i].x = live && n < N ? Arow[n] : 0.f;
+        A[e][i].y = live && n + 1 < N ? Arow[n + 1] : 0.f;
+      }
+    const float fbias = p.f.dt_bias ? p.f.dt_bias[cf] : 0.f, skip = p.f.Dskip ? p.f.Dskip[cf] : 0.f;
+    piece_wait<0>();
+    __syncthreads();
+    {
+      const int cc = lane % CH;                        // a lane's items have one channel
+      const bool con = wc + cc < k.cw;
+      const float bias = p.f.dt_bias && con ? p.f.dt_bias[k.c0 + wc + cc] : 0.f;
+#pragma unroll 4
+      for (int m = 0; m < SEG * CH / 32; ++m) {
+        const int t = (lane + m * 32) / CH;
+        const bool on = t0 + t < t_end && con;
+        const float d = softplus_f32(to_f32(sm.raw.d[t][cc]) + bias);
+        float dy = to_f32(sm.raw.o[t][cc]);
+        if (p.f.z) {
+          const float z = to_f32(sm.raw.z[t][cc]);
+          dy *= z * sigmoid_f32(z);
+        }
+        sm.d[t][cc] = on ? d : 0.f;                    // past the end: the state and the adjoint stay
+        sm.dy[t][cc] = on ? dy : 0.f;
+      }
+    }
+    if (warp == 0) ssm_rows_f32<T, NP, SEG, true>(p.f, sb.raw.b, sb.raw.c, sb.bc, row0, k.g, t0, t_end, lane);
+    __syncthreads();                                   // the raw rows are used up
+
+    const int last = (t_end - t0 - 1) / GT;            // groups behind this one leave all as it is
+    // forward: the state before each group
+#pragma unroll 1
+    for (int gr = 0; gr < last; ++gr) {
 #pragma unroll
       for (int j = 0; j < GT; ++j) {
         const int t = gr * GT + j;
-        const float2 d = sm.d[t][ch];
-        float bv[NS], cv[NS];
-        lds_states<NS>(sm.b + t * 4 * NS + q * NS, bv);
-        lds_states<NS>(sm.c + t * 4 * NS + q * NS, cv);
-        yv[j] = 0.f;
+        const float2 d = ssm_pair(&sm.d[t][lc]), u = ssm_pair(&sm.u[t][lc]);
+        uint64_t b2[H2];
+        ssm_lds_pairs<H2>(&sb.bc[t][0][q * NH], b2);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          a[j][i] = ex2_approx(d.x * (A[i] * 1.4426950408889634f));
-          ah[j][i] = a[j][i] * h[i];
-          h[i] = fmaf(d.y, bv[i], ah[j][i]);
-          yv[j] = fmaf(h[i], cv[i], yv[j]);
+        for (int e = 0; e < 2; ++e) {
+          const float de = e ? d.y : d.x, due = de * (e ? u.y : u.x), dl = de * 1.4426950408889634f;
+          const uint64_t d2 = f32x2_pack(dl, dl), du2 = f32x2_pack(due, due);
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            const float2 x = f32x2_unpack(fmul2(d2, f32x2_pack(A[e][i])));
+            const uint64_t a = f32x2_pack(ex2_approx(x.x), ex2_approx(x.y));
+            h[e][i] = f32x2_unpack(ffma2(a, f32x2_pack(h[e][i]), fmul2(du2, b2[i])));
+          }
         }
+      }
+#pragma unroll
+      for (int i = 0; i < H2; ++i) sm.ck.h[gr][i][lane] = make_float4(h[0][i].x, h[0][i].y, h[1][i].x, h[1][i].y);
+    }
+    // where dB and dC of this lane's share go, and where the block's sums go
+    int at = 0;
+    int buf = 0;
+    const long long cb = static_cast<long long>(k.g) * p.cbg + (k.c0 - k.g * p.f.Dg) / Cfg::BCH;
+    float* part = p.part_bc + ((cb * p.f.B + k.b) * p.f.L + t0) * 2 * N;
+    // backward, last group first
+#pragma unroll 1
+    for (int gr = last; gr >= 0; --gr, buf ^= 1) {
+      // what finishing the group's rows reads again
+      const int ft = gr * GT + (SPL > 2 ? q / 2 * FT : 0);   // the first row this lane finishes
+      const long long fo = (row0 + t0 + ft) * p.f.D + cf;
+      T rd[FT], ro[FT], rz[FT];
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        if (live && t0 + ft + j < t_end) {
+          rd[j] = static_cast<const T*>(p.f.dt)[fo + j * static_cast<long long>(p.f.D)];
+          ro[j] = static_cast<const T*>(p.dout)[fo + j * static_cast<long long>(p.f.D)];
+          if (p.f.z) rz[j] = static_cast<const T*>(p.f.z)[fo + j * static_cast<long long>(p.f.D)];
+        }
+      if (gr > 0) {
+#pragma unroll
+        for (int i = 0; i < H2; ++i) {
+          const float4 v = sm.ck.h[gr - 1][i][lane];
+          h[0][i] = make_float2(v.x, v.y);
+          h[1][i] = make_float2(v.z, v.w);
+        }
+      } else {
+        load_pairs(seg_h, h);
+      }
+      uint64_t a[GT][2][H2], ah[GT][2][H2];
+      float yv[GT][2], xv[GT][2], sv[GT][2], vc[GT];
+#pragma unroll
+      for (int j = 0; j < GT; ++j) {
+        const int t = gr * GT + j;
+        const float2 d = ssm_pair(&sm.d[t][lc]), u = ssm_pair(&sm.u[t][lc]), dy = ssm_pair(&sm.dy[t][lc]);
+        uint64_t b2[H2], c2[H2], qc[H2];
+        ssm_lds_pairs<H2>(&sb.bc[t][0][q * NH], b2);
+        ssm_lds_pairs<H2>(&sb.bc[t][1][q * NH], c2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float de = e ? d.y : d.x, due = de * (e ? u.y : u.x), dl = de * 1.4426950408889634f;
+          const float dye = e ? dy.y : dy.x;
+          const uint64_t d2 = f32x2_pack(dl, dl), du2 = f32x2_pack(due, due), dy2 = f32x2_pack(dye, dye);
+          uint64_t y2 = 0;
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            const float2 x = f32x2_unpack(fmul2(d2, f32x2_pack(A[e][i])));
+            a[j][e][i] = f32x2_pack(ex2_approx(x.x), ex2_approx(x.y));
+            ah[j][e][i] = fmul2(a[j][e][i], f32x2_pack(h[e][i]));
+            const uint64_t hn = ffma2(du2, b2[i], ah[j][e][i]);
+            h[e][i] = f32x2_unpack(hn);
+            y2 = i ? ffma2(hn, c2[i], y2) : fmul2(hn, c2[i]);
+            qc[i] = e ? ffma2(dy2, hn, qc[i]) : fmul2(dy2, hn);
+          }
+          const float2 y = f32x2_unpack(y2);
+          yv[j][e] = y.x + y.y;
+        }
+        float cs[NH];
+#pragma unroll
+        for (int i = 0; i < H2; ++i) f32x2_unpack(qc[i], cs[2 * i], cs[2 * i + 1]);
+        vc[j] = ssm_sum_lanes<NH>(cs, lane, Cfg::SPLIT ? 2 * SPL : SPL, at);
       }
 #pragma unroll
       for (int j = GT - 1; j >= 0; --j) {
         const int t = gr * GT + j;
-        const float2 d = sm.d[t][ch];
-        const float dy = sm.dy[t][ch];
-        float bv[NS], cv[NS], bc[2 * NS];
-        lds_states<NS>(sm.b + t * 4 * NS + q * NS, bv);
-        lds_states<NS>(sm.c + t * 4 * NS + q * NS, cv);
-        xv[j] = sv[j] = 0.f;
+        const float2 d = ssm_pair(&sm.d[t][lc]), u = ssm_pair(&sm.u[t][lc]), dy = ssm_pair(&sm.dy[t][lc]);
+        uint64_t b2[H2], c2[H2], qb[H2];
+        ssm_lds_pairs<H2>(&sb.bc[t][0][q * NH], b2);
+        ssm_lds_pairs<H2>(&sb.bc[t][1][q * NH], c2);
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          g[i] = fmaf(dy, cv[i], g[i]);
-          bc[i] = live ? g[i] * d.y : 0.f;
-          bc[NS + i] = live ? dy * fmaf(d.y, bv[i], ah[j][i]) : 0.f;
-          xv[j] = fmaf(g[i], bv[i], xv[j]);
-          const float w = g[i] * ah[j][i];
-          sv[j] = fmaf(w, A[i], sv[j]);
-          dA[i] = fmaf(w, d.x, dA[i]);
-          g[i] *= a[j][i];
+        for (int e = 0; e < 2; ++e) {
+          const float de = e ? d.y : d.x, due = de * (e ? u.y : u.x), dye = e ? dy.y : dy.x;
+          const uint64_t d2 = f32x2_pack(de, de), du2 = f32x2_pack(due, due), dy2 = f32x2_pack(dye, dye);
+          uint64_t x2 = 0, s2 = 0;
+#pragma unroll
+          for (int i = 0; i < H2; ++i) {
+            const uint64_t gn = ffma2(dy2, c2[i], f32x2_pack(g[e][i]));
+            qb[i] = e ? ffma2(du2, gn, qb[i]) : fmul2(du2, gn);
+            x2 = i ? ffma2(gn, b2[i], x2) : fmul2(gn, b2[i]);
+            const uint64_t w = fmul2(gn, ah[j][e][i]);
+            s2 = i ? ffma2(w, f32x2_pack(A[e][i]), s2) : fmul2(w, f32x2_pack(A[e][i]));
+            dA[e][i] = f32x2_unpack(ffma2(w, d2, f32x2_pack(dA[e][i])));
+            g[e][i] = f32x2_unpack(fmul2(gn, a[j][e][i]));
+          }
+          const float2 x = f32x2_unpack(x2), s = f32x2_unpack(s2);
+          xv[j][e] = x.x + x.y;
+          sv[j][e] = s.x + s.y;
         }
-        // over the warp's 8 channels: lane bits 4, 3, 2 pick which sums are kept
-        constexpr int C0 = 2 * NS;
-        int at = 0;
-        if constexpr (C0 >= 2) {
-          halve_sum(bc, C0, 16, lane & 16);
-          at += lane & 16 ? C0 / 2 : 0;
-        }
-        if constexpr (C0 >= 4) {
-          halve_sum(bc, C0 / 2, 8, lane & 8);
-          at += lane & 8 ? C0 / 4 : 0;
+        float bs[NH];
+#pragma unroll
+        for (int i = 0; i < H2; ++i) f32x2_unpack(qb[i], bs[2 * i], bs[2 * i + 1]);
+        const float vb = ssm_sum_lanes<NH>(bs, lane, Cfg::SPLIT ? 2 * SPL : SPL, at);
+        // this warp's sums of dB and dC over its channels
+        float* red = &sb.red[buf][warp][j][q * NH + at];
+        if constexpr (Cfg::SPLIT) {                    // the last lane bit: one of the two is left to add
+          const bool up = lane & SPL;
+          red[up ? NP : 0] = (up ? vc[j] : vb) + __shfl_xor_sync(0xffffffffu, up ? vb : vc[j], SPL);
         } else {
-          bc[0] += __shfl_xor_sync(0xffffffffu, bc[0], 8);
+          red[0] = vb;
+          red[NP] = vc[j];
         }
-        if constexpr (C0 >= 8) {
-          halve_sum(bc, C0 / 4, 4, lane & 4);
-          at += lane & 4 ? C0 / 8 : 0;
-        } else {
-          bc[0] += __shfl_xor_sync(0xffffffffu, bc[0], 4);
+      }
+      // y, dx, sum w A over the lanes of a channel: bit 0 picks the channel, bit 1 (if any) the tokens
+#pragma unroll
+      for (int j = 0; j < GT; ++j) {
+        halve_sum(yv[j], 2, 1, q & 1);
+        halve_sum(xv[j], 2, 1, q & 1);
+        halve_sum(sv[j], 2, 1, q & 1);
+      }
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        float fy = yv[j][0], fx = xv[j][0], fs = sv[j][0];
+        if constexpr (SPL == 4) {
+          const bool up = q & 2;
+          fy = (up ? yv[j + FT][0] : fy) + __shfl_xor_sync(0xffffffffu, up ? fy : yv[j + FT][0], 2);
+          fx = (up ? xv[j + FT][0] : fx) + __shfl_xor_sync(0xffffffffu, up ? fx : xv[j + FT][0], 2);
+          fs = (up ? sv[j + FT][0] : fs) + __shfl_xor_sync(0xffffffffu, up ? fs : sv[j + FT][0], 2);
         }
-        constexpr int KEEP = C0 >= 8 ? C0 / 8 : 1;
-#pragma unroll
-        for (int i = 0; i < KEEP; ++i) sm.red[warp][j][q * C0 + at + i] = bc[i];
+        const int tl = ft + j;
+        if (live && t0 + tl < t_end) {
+          const float u = to_f32(sm.u[tl][fc]), d = sm.d[tl][fc], dy = sm.dy[tl][fc];
+          const float ddt = fmaf(fx, u, fs) * sigmoid_f32(to_f32(rd[j]) + fbias);
+          const long long o = fo + j * static_cast<long long>(p.f.D);
+          static_cast<T*>(p.du)[o] = from_f32<T>(fmaf(fx, d, skip * dy));
+          static_cast<T*>(p.ddt)[o] = from_f32<T>(ddt);
+          sD = fmaf(dy, u, sD);
+          sT += ddt;
+          if (p.f.z) {
+            const float z = to_f32(rz[j]), s = sigmoid_f32(z);
+            static_cast<T*>(p.dz)[o] = from_f32<T>(to_f32(ro[j]) * fmaf(skip, u, fy) * (s * fmaf(z, 1.f - s, 1.f)));
+          }
+        }
       }
-      // y, dx, sum w A: over the 4 state quarters; lane q keeps GT / 4 tokens from q GT / 4
-      halve_sum(yv, GT, 2, q & 2);
-      halve_sum(yv, GT / 2, 1, q & 1);
-      halve_sum(xv, GT, 2, q & 2);
-      halve_sum(xv, GT / 2, 1, q & 1);
-      halve_sum(sv, GT, 2, q & 2);
-      halve_sum(sv, GT / 2, 1, q & 1);
-      __syncwarp();                              // the warp is done with the group's d and dy
-#pragma unroll
-      for (int i = 0; i < GT / 4; ++i) {
-        const int t = gr * GT + q * (GT / 4) + i;
-        sm.d[t][ch] = make_float2(xv[i], sv[i]);
-        sm.dy[t][ch] = yv[i];
-      }
+      // the block's sums of dB and dC; the next group's go to the other buffer, and the one after comes
+      // behind this barrier's successor
       __syncthreads();
-      for (int i = tid; i < GT * 8 * NS; i += SSM_THREADS) {
-        const int j = i / (8 * NS), e = i - j * (8 * NS);
-        const int qq = e / (2 * NS), f = e - qq * (2 * NS);   // quarter; dB_0.., dC_0..
-        const int n = qq * NS + (f < NS ? f : f - NS), t = t0 + gr * GT + j;
+      for (int i = threadIdx.x; i < GT * 2 * NP; i += SSM_THREADS) {
+        const int j = i / (2 * NP), f = i % (2 * NP), n = f % NP, t = gr * GT + j;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < SSM_THREADS / 32; ++w) s += sm.red[w][j][e];
-        if (n < N && t < t_end) {
-          const long long cb = k.g * p.f.cbg + (k.c0 - k.g * p.f.Dg) / SSM_CH;
-          const long long row = (cb * p.f.B + k.b) * p.f.L + t;
-          p.part_bc[row * 2 * N + (f < NS ? n : N + n)] = s;
-        }
-      }
-      __syncthreads();                           // the sums are read before the next group's
-    }
-    // whole rows: du, ddt, dz, and the sums over tokens of dDskip, ddt_bias
-    float sD[V], sT[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) sD[i] = sT[i] = 0.f;
-    for (int it = tid; it < Cfg::SEG * CPR; it += SSM_THREADS) {
-      const int t = it / CPR, cc = it % CPR * V;
-      if (t0 + t < t_end && cc < k.cw) {
-        const long long at = (static_cast<long long>(k.b) * p.f.L + t0 + t) * p.f.D + k.c0 + cc;
-        VecPack<T, V> u, d, z, o, ou, od, oz;
-        u.load(static_cast<const T*>(p.f.u) + at);
-        d.load(static_cast<const T*>(p.f.dt) + at);
-        o.load(static_cast<const T*>(p.dout) + at);
-        if (p.f.z) z.load(static_cast<const T*>(p.f.z) + at);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float bias = p.f.dt_bias ? p.f.dt_bias[k.c0 + cc + i] : 0.f;
-          const float skip = p.f.Dskip ? p.f.Dskip[k.c0 + cc + i] : 0.f;
-          const float raw = to_f32(d.e[i]) + bias, dl = softplus_f32(raw), uf = to_f32(u.e[i]);
-          const float2 xs = sm.d[t][cc + i];
-          float dy = to_f32(o.e[i]);
-          if (p.f.z) {
-            const float zf = to_f32(z.e[i]), sg = sigmoid_f32(zf);
-            const float y = fmaf(skip, uf, sm.dy[t][cc + i]);
-            oz.e[i] = from_f32<T>(dy * y * (sg * fmaf(zf, 1.f - sg, 1.f)));
-            dy *= zf * sg;
-          }
-          const float dt = fmaf(xs.x, uf, xs.y) * sigmoid_f32(raw);
-          ou.e[i] = from_f32<T>(fmaf(xs.x, dl, skip * dy));
-          od.e[i] = from_f32<T>(dt);
-          sD[i] = fmaf(dy, uf, sD[i]);
-          sT[i] += dt;
-        }
-        ou.store(static_cast<T*>(p.du) + at);
-        od.store(static_cast<T*>(p.ddt) + at);
-        if (p.f.z) oz.store(static_cast<T*>(p.dz) + at);
+        for (int w = 0; w < SSM_THREADS / 32; ++w) s += sb.red[buf][w][j][f];
+        if (n < N && t0 + t < t_end) part[t * 2 * N + (f < NP ? n : N + n)] = s;
       }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      sm.cs[0][tid / CPR][tid % CPR * V + i] = sD[i];
-      sm.cs[1][tid / CPR][tid % CPR * V + i] = sT[i];
-    }
-    __syncthreads();
-    if (tid < 2 * SSM_CH) {
-      const int w = tid / SSM_CH, cc = tid % SSM_CH;
-      float s = 0.f;
-      for (int i = 0; i < SSM_THREADS / CPR; ++i) s += sm.cs[w][i][cc];
-      if (cc < k.cw)
-        p.part_c[((static_cast<long long>(k.b) * p.f.nseg + k.s) * 2 + w) * p.f.D + k.c0 + cc] = s;
-    }
-  } else if (tid < 2 * SSM_CH && tid % SSM_CH < k.cw) {
-    p.part_c[((static_cast<long long>(k.b) * p.f.nseg + k.s) * 2 + tid / SSM_CH) * p.f.D + k.c0 +
-             tid % SSM_CH] = 0.f;
   }
-  // this segment's dA takes the place of its entering state, which only this block reads
-  if (live) ssm_store_states<NS>(p.f.seg_h + r * N, q, N, dA);
+  if constexpr (SPL > 2) {                             // lanes that finished other tokens of the channel
+    sD += __shfl_xor_sync(0xffffffffu, sD, 2);
+    sT += __shfl_xor_sync(0xffffffffu, sT, 2);
+  }
+  if (!live) return;
+  if (q < 2) {
+    float* pc = p.part_c + seg * 2 * p.f.D + cf;
+    pc[0] = sD;
+    pc[p.f.D] = sT;
+  }
+  // this segment's dA takes the place of its entering state, which only this warp reads
+#pragma unroll
+  for (int i = 0; i < H2; ++i) {
+    *reinterpret_cast<float2*>(seg_h + static_cast<long long>(2 * i) * p.f.D) = make_float2(dA[0][i].x, dA[1][i].x);
+    *reinterpret_cast<float2*>(seg_h + static_cast<long long>(2 * i + 1) * p.f.D) = make_float2(dA[0][i].y, dA[1][i].y);
+  }
 }
 
 // dB, dC [B][L][G][N] from the channel blocks' sums; rows past a sequence's end are left.
@@ -838,29 +990,29 @@ __global__ __launch_bounds__(256) void ssm_bwd_bc_kernel(const SsmBwdParams p) {
   const int b = static_cast<int>(row / p.f.L);
   if (p.f.lens && row - static_cast<long long>(b) * p.f.L >= seq_len(p.f.lens, b, p.f.L)) return;
   float s = 0.f;
-  const float* src = p.part_bc + (static_cast<long long>(g) * p.f.cbg * rows + row) * 2 * N + f;
+  const float* src = p.part_bc + (static_cast<long long>(g) * p.cbg * rows + row) * 2 * N + f;
 #pragma unroll 8
-  for (int i = 0; i < p.f.cbg; ++i) s += src[i * rows * 2 * N];
+  for (int i = 0; i < p.cbg; ++i) s += src[i * rows * 2 * N];
   T* dst = static_cast<T*>(f < N ? p.dB : p.dC);
   dst[(row * G + g) * N + (f < N ? f : f - N)] = from_f32<T>(s);
 }
 
 // dA [D][N], dDskip [D], ddt_bias [D]: sums over sequences and segments in a fixed order, 32 columns
 // x 8 lanes of segments per block.
-__global__ __launch_bounds__(256) void ssm_bwd_param_kernel(const SsmBwdParams p) {
+__global__ __launch_bounds__(256) void ssm_bwd_param_kernel(const SsmBwdParams p, int NP) {
   __shared__ float red[8][33];
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const long long nA = static_cast<long long>(p.f.D) * p.f.N, nC = 2LL * p.f.D;
+  const long long nA = static_cast<long long>(p.f.D) * p.f.N, nC = 2LL * p.f.D;   // columns [N][D], [2][D]
   const long long blocksA = (nA + 31) / 32;
   const bool isA = blockIdx.x < blocksA;
   const long long i = (isA ? blockIdx.x : blockIdx.x - blocksA) * 32LL + x;
-  const long long n = isA ? nA : nC;
+  const long long n = isA ? nA : nC, step = isA ? static_cast<long long>(p.f.D) * NP : nC;
   const float* src = isA ? p.f.seg_h : p.part_c;
   float a = 0.f;
   if (i < n) {
     const long long R = static_cast<long long>(p.f.B) * p.f.nseg;
 #pragma unroll 4
-    for (long long r = y; r < R; r += 8) a += src[r * n + i];
+    for (long long r = y; r < R; r += 8) a += src[r * step + i];
   }
   red[y][x] = a;
   __syncthreads();
@@ -869,7 +1021,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_param_kernel(const SsmBwdParams p
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += red[j][x];
     if (isA)
-      p.dA[i] = s;
+      p.dA[i % p.f.D * p.f.N + i / p.f.D] = s;
     else if (i < p.f.D) {
       if (p.dD) p.dD[i] = s;
     } else if (p.ddt_bias) {
