@@ -341,11 +341,11 @@ int ssm_np(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : 32; }
 // state, then outputs), so a sequence stays whole once its warps give each of the SM's four
 // schedulers one (B 8, D 4,096, N 16: 551 us whole, 660 in two); with fewer, segments fill the four
 // warps that fit on each (B 4, L 2,048, D 2,048: 475 us whole, 202 in nine). A segment shorter
-// than 64 tokens costs more to start than it gains.
+// than 32 tokens costs as much to start as it gains (B 1, L 512, D 1,024: 37 us at 64, 26 at 32, 24 at 16).
 void ssm_plan(kta::SsmParams& p) {
   const long long warps = static_cast<long long>(p.B) * p.G * p.cbg;
   const long long one = 4LL * sm_count(), full = one * (ssm_np(p.N) > 16 ? 3 : 4);
-  long long n = warps >= one ? 1 : std::max<long long>(1, std::min<long long>(full / warps, p.L / 64));
+  long long n = warps >= one ? 1 : std::max<long long>(1, std::min<long long>(full / warps, p.L / 32));
   p.seg = static_cast<int>((p.L + n - 1) / n);
   p.seg = (p.seg + kta::SSM_TT - 1) / kta::SSM_TT * kta::SSM_TT;
   p.nseg = (p.L + p.seg - 1) / p.seg;

@@ -484,7 +484,7 @@ struct SsmLocalSmem {
 
 // One warp = 32 channels of a group over one segment, a lane all states of one channel.
 template <typename T, int NP>
-__global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_local_kernel(const SsmBwdParams p) {
+__global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 4) void ssm_bwd_local_kernel(const SsmBwdParams p) {
   using Smem = SsmLocalSmem<T, NP>;
   constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, STAGES = Smem::STAGES;
   extern __shared__ __align__(16) unsigned char ssm_smem[];

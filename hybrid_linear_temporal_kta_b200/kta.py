@@ -643,53 +643,62 @@ def rope_freqs(dims, *, base: float = 10000.0, scaling: str | None = None, facto
     return torch.tensor(out, dtype=torch.float64, device=device), float(m.value)
 
 
+_Int4 = ctypes.c_int * 4
+
+
 def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, stream):
-    ty, dt, dev, _ = _io(q, "q", 4)
-    B, N, _, d = q.shape
+    ty, dt, dev, at_q = _io(q, "q", 4)
+    shape = q.shape
+    B, N, Hq, d = shape
     dims = (dims,) if isinstance(dims, int) else tuple(dims)
     A = len(dims)
     if not 1 <= A <= 4:
         raise ValueError("1 to 4 axes")
-    if layout not in ("half", "interleaved"):
+    if layout != "half" and layout != "interleaved":
         raise ValueError('layout must be "half" or "interleaved"')
     f = _want(freqs, "freqs", torch.float64, (sum(dims) // 2,), dev)
     per_seq, at = 0, None
     if pos is not None:
-        shape = pos.shape
-        if shape == (B, N, A) or (A == 1 and shape == (B, N)):
+        ps = pos.shape
+        if ps == (B, N, A) or (A == 1 and ps == (B, N)):
             per_seq = 1
-        elif not (shape == (N, A) or (A == 1 and shape == (N,))):
+        elif not (ps == (N, A) or (A == 1 and ps == (N,))):
             raise ValueError(f"pos must be [N, axes] or [B, N, axes] (one axis: [N] or [B, N]), got "
-                             f"{tuple(shape)}")
-        at = _want(pos, "pos", torch.int64, shape, dev)
-    xs = (q,) if k is None else (q, k)
-    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != d):
-        raise ValueError("k must have q's batch, tokens and head dim")
+                             f"{tuple(ps)}")
+        at = _want(pos, "pos", torch.int64, ps, dev)
+    Hk, at_k, shape_k = 0, None, None
+    if k is not None:
+        shape_k = k.shape
+        if len(shape_k) != 4 or shape_k[0] != B or shape_k[1] != N or shape_k[3] != d:
+            raise ValueError("k must have q's batch, tokens and head dim")
+        Hk, at_k = shape_k[2], _want(k, "k", ty, shape_k, dev)
+    off, nq, nk = 0, Hq, Hk
+    if heads is not None:
+        h0, h1 = heads
+        if not 0 <= h0 < h1 <= (Hq if k is None else min(Hq, Hk)):
+            raise ValueError(f"heads {heads} outside the tensors' heads")
+        off, nq, nk = h0 * d * q.element_size(), h1 - h0, h1 - h0
     if out is not None:
         out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(out) != len(xs):
+        if len(out) != (1 if k is None else 2):
             raise ValueError("out must have one tensor for each input")
-    cfg = Rope(A, (ctypes.c_int * 4)(*dims), begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
+        _want(out[0], "out", ty, shape, dev)
+        if k is not None:
+            _want(out[1], "out", ty, shape_k, dev)
+    cfg = Rope(A, _Int4(*dims), begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
 
     def body(st):
-        ptr, hs, os = [], [], []
-        for i, x in enumerate(xs):
-            H = x.shape[2]
-            h0, h1 = (0, H) if heads is None else heads
-            if not 0 <= h0 < h1 <= H:
-                raise ValueError(f"heads {heads} outside 0..{H}")
-            o = torch.empty_like(x) if out is None else out[i]
-            off = h0 * d * x.element_size()
-            ptr += (_want(x, "qk"[i], ty, x.shape, dev) + off, _want(o, "out", ty, x.shape, dev) + off)
-            hs += (h1 - h0, H)
-            os.append(o)
+        oq = torch.empty_like(q) if out is None else out[0]
         if k is None:
-            ptr += (None, None)
-            hs += (0, 0)
-        _check(fn(ctypes.byref(cfg), *ptr, Shape(B, 1, N, d, dt), *hs, st), fn.__name__)
-        return os[0] if k is None else tuple(os)
+            _check(fn(ctypes.byref(cfg), at_q + off, oq.data_ptr() + off, None, None,
+                      Shape(B, 1, N, d, dt), nq, Hq, 0, 0, st), "kta_rope")
+            return oq
+        ok = torch.empty_like(k) if out is None else out[1]
+        _check(fn(ctypes.byref(cfg), at_q + off, oq.data_ptr() + off, at_k + off, ok.data_ptr() + off,
+                  Shape(B, 1, N, d, dt), nq, Hq, nk, Hk, st), "kta_rope")
+        return oq, ok
 
-    return _launch(dev, stream, body, xs + (freqs, pos) + (out or ()))
+    return _launch(dev, stream, body, (q, k, freqs, pos) + (out or ()))
 
 
 def rope_fwd(q, k=None, *, freqs, dims, begin: int = 0, layout: str = "half", mscale: float = 1.0,
@@ -732,11 +741,12 @@ def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
     (fresh buffers are zero there) and the end state is taken there. Returns o (and the last K - 1
     rows)."""
     c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
+    _want(out, "out", ty, x.shape, dev)
 
     def body(st):
         o = _fresh(x, lens) if out is None else out
         S = torch.empty((c.B, c.K - 1, c.D), device=x.device, dtype=ty) if return_state else None
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _want(o, "out", ty, x.shape, dev),
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), o.data_ptr(),
                                        None if S is None else S.data_ptr(), st), "kta_short_conv_fwd")
         return (o, S) if return_state else o
 
@@ -751,11 +761,11 @@ def short_conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None
         raise ValueError("state must be a tensor")
     c, ty, dev = _conv_args(x, w, bias, silu, state, None, step=True)
     end = c.S0 if state_out is None else _want(state_out, "state_out", ty, state.shape, dev)
+    _want(out, "out", ty, x.shape, dev)
 
     def body(st):
         o = torch.empty_like(x) if out is None else out
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), _want(o, "out", ty, x.shape, dev), end, st),
-               "kta_short_conv_fwd")
+        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), o.data_ptr(), end, st), "kta_short_conv_fwd")
         return o
 
     return _launch(dev, stream, body, (x, w, bias, state, state_out, out))
@@ -769,6 +779,7 @@ def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=No
     c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
     g = _want(dout, "dout", ty, x.shape, dev)
     e = _want(dS_out, "dS_out", ty, (c.B, c.K - 1, c.D), dev)
+    _want(out, "out", ty, x.shape, dev)
 
     def body(st):
         dx = _fresh(x, lens) if out is None else out
@@ -778,7 +789,7 @@ def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=No
         n = _lib.kta_short_conv_bwd_workspace(ctypes.byref(c))
         ws = _scratch(n, x)
         _check(_lib.kta_short_conv_bwd(
-            ctypes.byref(c), g, e, _want(dx, "out", ty, x.shape, dev), dw.data_ptr(),
+            ctypes.byref(c), g, e, dx.data_ptr(), dw.data_ptr(),
             None if dbias is None else dbias.data_ptr(), None if dS0 is None else dS0.data_ptr(),
             None if ws is None else ws.data_ptr(), n, st), "kta_short_conv_bwd")
         return dx, dw, dbias, dS0
@@ -810,13 +821,14 @@ def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, len
     [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
     end state is taken there. Returns y (and the end state)."""
     c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    _want(out, "out", ty, u.shape, dev)
 
     def body(st):
         y = _fresh(u, lens) if out is None else out
         S = torch.empty((c.B, c.D, c.N), device=u.device, dtype=torch.float32) if return_state else None
         n = _lib.kta_ssm_scan_fwd_workspace(ctypes.byref(c))
         ws = _scratch(n, u)
-        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), _want(y, "out", ty, u.shape, dev),
+        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), y.data_ptr(),
                                      None if S is None else S.data_ptr(),
                                      None if ws is None else ws.data_ptr(), n, st), "kta_ssm_scan_fwd")
         return (y, S) if return_state else y
@@ -832,11 +844,11 @@ def ssm_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, stat
         raise ValueError("state must be a tensor")
     c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
     end = c.S0 if state_out is None else _want(state_out, "state_out", torch.float32, state.shape, dev)
+    _want(out, "out", ty, u.shape, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out
-        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), _want(y, "out", ty, u.shape, dev), end, st),
-               "kta_ssm_scan_step")
+        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), y.data_ptr(), end, st), "kta_ssm_scan_step")
         return y
 
     return _launch(dev, stream, body, (u, dt, A, Bm, Cm, D, z, dt_bias, state, state_out, out))
