@@ -391,12 +391,11 @@ kta_status launch_ssm_fwd(const kta::SsmParams& p, cudaStream_t st) {
 
 template <typename T, int NS>
 kta_status launch_ssm_step(const kta::SsmParams& p, cudaStream_t st) {
-  const long long items = static_cast<long long>((p.B + kta::SSM_STEP_B - 1) / kta::SSM_STEP_B) * p.D * 4;
-  const long long blocks = (items + kta::SSM_THREADS - 1) / kta::SSM_THREADS;
-  kta_status r;
-  if ((r = check_grid(blocks))) return r;
+  const int gy = (p.B + kta::SSM_STEP_B - 1) / kta::SSM_STEP_B;
+  if (gy > 65535) return fail(KTA_ERR_UNSUPPORTED, "a step takes at most %d sequences", 65535 * kta::SSM_STEP_B);
+  const dim3 grid((static_cast<unsigned>(p.D) * 4 + kta::SSM_THREADS - 1) / kta::SSM_THREADS, static_cast<unsigned>(gy));
   TraceScope ts("ssm_step", st);
-  kta::ssm_step_kernel<T, NS><<<static_cast<unsigned>(blocks), kta::SSM_THREADS, 0, st>>>(p);
+  kta::ssm_step_kernel<T, NS><<<grid, kta::SSM_THREADS, 0, st>>>(p);
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }

@@ -268,6 +268,7 @@ __global__ __launch_bounds__(SC_BWD_X* SC_BWD_Y, 4) void short_conv_bwd_kernel(c
     for (; s < t1; ++s) row(s, true);
 #pragma unroll 1
     for (; s < s_end; ++s) row(s, false);     // the next run's first rows complete dx of this one's last
+    piece_wait<0>();
   }
   // sums over the block's runs, in run order
 #pragma unroll

@@ -478,7 +478,8 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
  *  - ws: kta_ssm_scan_fwd_workspace(c) bytes (asked with the same device current; may be 0), device
  *    memory, 16-byte aligned, for this call alone until it has run. A long sequence with few channels
  *    is cut into segments that run at once: their end states from zero are kept there.
- * kta_ssm_scan_step: one token (L = 1) from S0 to S_out; S_out = S0 updates in place; no workspace.
+ * kta_ssm_scan_step: one token (L = 1) from S0 to S_out; S_out = S0 updates in place; no workspace;
+ * B <= 131,070.
  *
  * kta_ssm_scan_bwd: gradients of sum(dout * y) + sum(dS_out * S_out). With dy_t = dout_t silu(z_t) and
  * G_t = dy_t C_t + exp(d_{t+1} A) G_{t+1} (behind the last token: dS_out or 0):
