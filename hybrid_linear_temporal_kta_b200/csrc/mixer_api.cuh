@@ -46,6 +46,24 @@ kta_status check_grid(long long blocks) {
   return KTA_OK;
 }
 
+// Launches a kernel that the one before it on the stream (of the same call) may start early: it waits
+// for that one's end itself, where it needs its results. The scan's backward gains 4 % (307 -> 295 us at
+// 2 x 2,048 x 2,048 x 16); its forward lost as much on short inputs and launches in order.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ------------------------------------------------------------------------- rotary
 
 template <typename T, bool HALF>
@@ -235,8 +253,7 @@ kta_status launch_conv_bwd(const kta::ConvParams& p, long long blocks, long long
   }
   TraceScope ts("short_conv_dw", st);
   const unsigned g = static_cast<unsigned>(((K + 1) * static_cast<long long>(p.D) + 31) / 32);
-  kta::short_conv_dw_kernel<K><<<g, 256, 0, st>>>(p.part, rows, p.D, dw, dbias);
-  KTA_CUDA(cudaGetLastError());
+  KTA_CUDA(launch_next(kta::short_conv_dw_kernel<K>, g, 256, 0, st, p.part, rows, p.D, dw, dbias));
   return KTA_OK;
 }
 
@@ -440,9 +457,11 @@ kta_status launch_ssm_bwd(const kta::SsmBwdParams& p, cudaStream_t st) {
   const long long blocks_l = (segs * p.f.cbg + W - 1) / W, blocks_m = segs * p.cbg;
   const long long states = static_cast<long long>(p.f.B) * p.f.D * NP;
   const long long bc = static_cast<long long>(p.f.B) * p.f.L * p.f.G * 2 * p.f.N;
+  const long long bc_blocks = (bc + 255) / 256;
+  const long long param_blocks = (static_cast<long long>(p.f.D) * p.f.N + 31) / 32 + (2LL * p.f.D + 31) / 32;
   kta_status r;
   if ((r = check_grid(blocks_l)) || (r = check_grid(blocks_m)) || (r = check_grid((states + 255) / 256)) ||
-      (r = check_grid((bc + 255) / 256)))
+      (r = check_grid(bc_blocks + param_blocks)))
     return r;
   const size_t smem_l = W * sizeof(kta::SsmLocalSmem<T, NP>), smem_m = sizeof(kta::SsmMainSmem<T, NP>);
   if ((r = set_smem_attr(kta::ssm_bwd_local_kernel<T, NP>, smem_l)) ||
@@ -455,24 +474,17 @@ kta_status launch_ssm_bwd(const kta::SsmBwdParams& p, cudaStream_t st) {
   }
   {
     TraceScope ts("ssm_bwd_carry", st);
-    kta::ssm_bwd_carry_kernel<<<dim3(static_cast<unsigned>((states + 255) / 256), 2), 256, 0, st>>>(p, NP);
-    KTA_CUDA(cudaGetLastError());
+    KTA_CUDA(launch_next(kta::ssm_bwd_carry_kernel, dim3(static_cast<unsigned>((states + 255) / 256), 2), 256, 0, st,
+                         p, NP));
   }
   {
     TraceScope ts("ssm_bwd_main", st);
-    kta::ssm_bwd_main_kernel<T, NP><<<static_cast<unsigned>(blocks_m), kta::SSM_THREADS, smem_m, st>>>(p);
-    KTA_CUDA(cudaGetLastError());
+    KTA_CUDA(launch_next(kta::ssm_bwd_main_kernel<T, NP>, static_cast<unsigned>(blocks_m), kta::SSM_THREADS, smem_m,
+                         st, p));
   }
-  {
-    TraceScope ts("ssm_bwd_bc", st);
-    kta::ssm_bwd_bc_kernel<T><<<static_cast<unsigned>((bc + 255) / 256), 256, 0, st>>>(p);
-    KTA_CUDA(cudaGetLastError());
-  }
-  TraceScope ts("ssm_bwd_param", st);
-  const long long nA = static_cast<long long>(p.f.D) * p.f.N;
-  const long long pb = (nA + 31) / 32 + (2LL * p.f.D + 31) / 32;
-  kta::ssm_bwd_param_kernel<<<static_cast<unsigned>(pb), 256, 0, st>>>(p, NP);
-  KTA_CUDA(cudaGetLastError());
+  TraceScope ts("ssm_bwd_sums", st);
+  KTA_CUDA(launch_next(kta::ssm_bwd_sums_kernel<T>, static_cast<unsigned>(bc_blocks + param_blocks), 256, 0, st, p,
+                       NP, static_cast<unsigned>(bc_blocks)));
   return KTA_OK;
 }
 

@@ -78,6 +78,12 @@ __device__ __forceinline__ float2 f32x2_unpack(uint64_t v) {
   return r;
 }
 
+// Kernels of one call in a row: a kernel lets the next be set up while it still runs, and the next one
+// waits, before it touches what the earlier ones write, until they have ended. Both do nothing in a
+// launch without the attribute.
+__device__ __forceinline__ void chain_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int BYTES>
 __device__ __forceinline__ void piece_async(void* dst, const void* src, bool on) {
   const uint32_t n = on ? BYTES : 0;       // 0: filled with zeros

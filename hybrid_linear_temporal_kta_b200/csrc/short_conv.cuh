@@ -155,6 +155,7 @@ __global__ __launch_bounds__(SC_BWD_X* SC_BWD_Y, 4) void short_conv_bwd_kernel(c
   constexpr int V = SC_V, P = V / 2;
   __shared__ typename VecPack<T, V>::Raw ring[SC_RING][2][SC_BWD_X * SC_BWD_Y];
   __shared__ __align__(16) float red[SC_BWD_Y][K + 1][SC_BWD_X * V + 4];
+  chain_start();
   const int xb = (p.nch + SC_BWD_X - 1) / SC_BWD_X, yb = (p.runs + SC_BWD_Y - 1) / SC_BWD_Y;
   const long long blk = blockIdx.x / xb;     // (sequence, block of runs)
   const int cx = static_cast<int>(blockIdx.x - blk * xb) * SC_BWD_X + (threadIdx.x % SC_BWD_X);
@@ -295,6 +296,7 @@ __global__ __launch_bounds__(256) void short_conv_dw_kernel(const float* part, l
                                                             float* dw, float* dbias) {
   __shared__ float red[8][33];
   const int n = (K + 1) * D, x = threadIdx.x % 32, y = threadIdx.x / 32;
+  chain_wait();
   const int i = blockIdx.x * 32 + x;
   float a = 0.f;
   if (i < n)

@@ -437,7 +437,7 @@ __global__ __launch_bounds__(SSM_THREADS) void ssm_step_kernel(const SsmParams p
 //  3. ssm_bwd_main: a forward walk keeps the state before every GT tokens in shared memory; then,
 //     last group first, the group's states are formed again in registers and the adjoint walks back:
 //     three exponentials per (token, channel, state) in all, and no state but the segments' in memory;
-//  4. ssm_bwd_bc, ssm_bwd_param: sums over channel blocks, and over segments, in a fixed order.
+//  4. ssm_bwd_sums: sums over channel blocks, and over segments, in a fixed order.
 
 template <int NP> struct SsmBwdCfg {
   static constexpr int NH = NP == 32 ? 8 : NP >= 8 ? 4 : 2;   // states of one lane, for each of two channels
@@ -490,6 +490,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 4) void ssm_bwd_local_ke
   constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, STAGES = Smem::STAGES;
   extern __shared__ __align__(16) unsigned char ssm_smem[];
   Smem& sm = reinterpret_cast<Smem*>(ssm_smem)[threadIdx.x / 32];
+  chain_start();
   const int lane = threadIdx.x % 32;
   const long long wid = blockIdx.x * static_cast<long long>(SSM_THREADS / 32) + threadIdx.x / 32;
   if (wid >= static_cast<long long>(p.f.B) * p.f.nseg * p.f.G * p.f.cbg) return;
@@ -590,6 +591,8 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 4) void ssm_bwd_local_ke
 // One thread per (sequence, state, channel), in place: local end states become entering states
 // (blockIdx.y 0), local adjoints the adjoints entering from behind (1).
 __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p, int NP) {
+  chain_start();
+  chain_wait();
   const long long per = static_cast<long long>(p.f.D) * NP;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (gid >= per * p.f.B) return;
@@ -709,6 +712,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
   static_assert(SPL == 2 || SPL == 4, "two or four lanes share a channel pair");
   extern __shared__ __align__(16) unsigned char ssm_smem[];
   Smem& sb = *reinterpret_cast<Smem*>(ssm_smem);
+  chain_start();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, q = lane % SPL, cp = lane / SPL, N = p.f.N;
   typename Smem::Warp& sm = sb.w[warp];
   const SsmBlock k = ssm_block(p.f, blockIdx.x, p.f.nseg, p.cbg, Cfg::BCH);
@@ -757,8 +761,6 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
         v[1][i] = make_float2(a.y, b.y);
       }
     };
-    load_pairs(seg_h, h);
-    load_pairs(sg, g);
 #pragma unroll
     for (int i = 0; i < H2; ++i)
 #pragma unroll
@@ -769,6 +771,9 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
         A[e][i].y = live && n + 1 < N ? Arow[n + 1] : 0.f;
       }
     const float fbias = p.f.dt_bias ? p.f.dt_bias[cf] : 0.f, skip = p.f.Dskip ? p.f.Dskip[cf] : 0.f;
+    chain_wait();
+    load_pairs(seg_h, h);
+    load_pairs(sg, g);
     piece_wait<0>();
     __syncthreads();
     {
@@ -962,6 +967,7 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
       }
     }
   }
+  if (t0 >= t_end) chain_wait();                       // (it has no states to load, but one to write over)
   if constexpr (SPL > 2) {                             // lanes that finished other tokens of the channel
     sD += __shfl_xor_sync(0xffffffffu, sD, 2);
     sT += __shfl_xor_sync(0xffffffffu, sT, 2);
@@ -980,40 +986,41 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
   }
 }
 
-// dB, dC [B][L][G][N] from the channel blocks' sums; rows past a sequence's end are left.
+// The call's last launch. Its first `bc_blocks` blocks: dB, dC [B][L][G][N] from the channel blocks' sums;
+// rows past a sequence's end are left. The others: dA [D][N], dDskip [D], ddt_bias [D], sums over
+// sequences and segments, 32 columns x 8 lanes of segments per block. All in a fixed order.
 template <typename T>
-__global__ __launch_bounds__(256) void ssm_bwd_bc_kernel(const SsmBwdParams p) {
-  const int N = p.f.N, G = p.f.G;
-  const long long rows = static_cast<long long>(p.f.B) * p.f.L;
-  const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const long long row = gid / (2 * N * G);
-  if (row >= rows) return;
-  const int e = static_cast<int>(gid - row * (2 * N * G)), g = e / (2 * N), f = e - g * (2 * N);
-  const int b = static_cast<int>(row / p.f.L);
-  if (p.f.lens && row - static_cast<long long>(b) * p.f.L >= seq_len(p.f.lens, b, p.f.L)) return;
-  float s = 0.f;
-  const float* src = p.part_bc + (static_cast<long long>(g) * p.cbg * rows + row) * 2 * N + f;
-#pragma unroll 8
-  for (int i = 0; i < p.cbg; ++i) s += src[i * rows * 2 * N];
-  T* dst = static_cast<T*>(f < N ? p.dB : p.dC);
-  dst[(row * G + g) * N + (f < N ? f : f - N)] = from_f32<T>(s);
-}
-
-// dA [D][N], dDskip [D], ddt_bias [D]: sums over sequences and segments in a fixed order, 32 columns
-// x 8 lanes of segments per block.
-__global__ __launch_bounds__(256) void ssm_bwd_param_kernel(const SsmBwdParams p, int NP) {
+__global__ __launch_bounds__(256) void ssm_bwd_sums_kernel(const SsmBwdParams p, int NP, unsigned bc_blocks) {
   __shared__ float red[8][33];
+  const int N = p.f.N, G = p.f.G;
+  chain_wait();
+  if (blockIdx.x < bc_blocks) {
+    const long long rows = static_cast<long long>(p.f.B) * p.f.L;
+    const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long row = gid / (2 * N * G);
+    if (row >= rows) return;
+    const int e = static_cast<int>(gid - row * (2 * N * G)), g = e / (2 * N), f = e - g * (2 * N);
+    const int b = static_cast<int>(row / p.f.L);
+    if (p.f.lens && row - static_cast<long long>(b) * p.f.L >= seq_len(p.f.lens, b, p.f.L)) return;
+    float s = 0.f;
+    const float* src = p.part_bc + (static_cast<long long>(g) * p.cbg * rows + row) * 2 * N + f;
+#pragma unroll 8
+    for (int i = 0; i < p.cbg; ++i) s += src[i * rows * 2 * N];
+    T* dst = static_cast<T*>(f < N ? p.dB : p.dC);
+    dst[(row * G + g) * N + (f < N ? f : f - N)] = from_f32<T>(s);
+    return;
+  }
   const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const long long nA = static_cast<long long>(p.f.D) * p.f.N, nC = 2LL * p.f.D;   // columns [N][D], [2][D]
-  const long long blocksA = (nA + 31) / 32;
-  const bool isA = blockIdx.x < blocksA;
-  const long long i = (isA ? blockIdx.x : blockIdx.x - blocksA) * 32LL + x;
+  const long long nA = static_cast<long long>(p.f.D) * N, nC = 2LL * p.f.D;   // columns [N][D], [2][D]
+  const long long blocksA = (nA + 31) / 32, blk = blockIdx.x - bc_blocks;
+  const bool isA = blk < blocksA;
+  const long long i = (isA ? blk : blk - blocksA) * 32 + x;
   const long long n = isA ? nA : nC, step = isA ? static_cast<long long>(p.f.D) * NP : nC;
   const float* src = isA ? p.f.seg_h : p.part_c;
   float a = 0.f;
   if (i < n) {
     const long long R = static_cast<long long>(p.f.B) * p.f.nseg;
-#pragma unroll 4
+#pragma unroll 8
     for (long long r = y; r < R; r += 8) a += src[r * step + i];
   }
   red[y][x] = a;
@@ -1023,7 +1030,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_param_kernel(const SsmBwdParams p
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += red[j][x];
     if (isA)
-      p.dA[i % p.f.D * p.f.N + i / p.f.D] = s;
+      p.dA[i % p.f.D * N + i / p.f.D] = s;
     else if (i < p.f.D) {
       if (p.dD) p.dD[i] = s;
     } else if (p.ddt_bias) {
