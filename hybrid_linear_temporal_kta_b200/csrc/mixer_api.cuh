@@ -66,20 +66,15 @@ cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem
 
 // ------------------------------------------------------------------------- rotary
 
-template <typename T, bool HALF>
-kta_status launch_rope(const kta::RopeParams& p, int V, dim3 grid, cudaStream_t st) {
+template <typename T>
+kta_status launch_rope(const kta::RopeParams& p, int W, dim3 grid, cudaStream_t st) {
   const size_t smem = static_cast<size_t>(p.tt) * (p.rot / 2) * sizeof(float2);
   TraceScope ts("rope", st);
-  constexpr int VMAX = 16 / int(sizeof(T));
-  if (V == VMAX)
-    kta::rope_kernel<T, VMAX, HALF><<<grid, kta::ROPE_THREADS, smem, st>>>(p);
-  else if constexpr (HALF) {
-    if constexpr (VMAX == 8) {
-      if (V == 4) kta::rope_kernel<T, 4, HALF><<<grid, kta::ROPE_THREADS, smem, st>>>(p);
-    }
-    if (V == 2) kta::rope_kernel<T, 2, HALF><<<grid, kta::ROPE_THREADS, smem, st>>>(p);
-    if (V == 1) kta::rope_kernel<T, 1, HALF><<<grid, kta::ROPE_THREADS, smem, st>>>(p);
-  }
+  auto kern = W == 0 ? kta::rope_kernel<T, 0> : W == 1 ? kta::rope_kernel<T, 1> : W == 2 ? kta::rope_kernel<T, 2>
+                                                                                   : kta::rope_kernel<T, 4>;
+  if constexpr (sizeof(T) == 2)
+    if (W == 8) kern = kta::rope_kernel<T, 8>;
+  kern<<<grid, kta::ROPE_THREADS, smem, st>>>(p);
   KTA_CUDA(cudaGetLastError());
   return KTA_OK;
 }
@@ -114,14 +109,12 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
   const void* xs[2] = {x, x2};
   void* os[2] = {o, o2};
   const int Hs[2] = {H, two ? H2 : 0}, lds[2] = {ld_heads, two ? ld_heads2 : 0};
-  bool copies = false;
   for (int w = 0; w < 2; ++w) {
     p.x[w] = xs[w];
     p.o[w] = os[w];
     p.H[w] = Hs[w];
     p.ld[w] = static_cast<long long>(lds[w]) * s.d;
     p.copy[w] = xs[w] != os[w] && rot < s.d;
-    copies = copies || (Hs[w] && p.copy[w]);
   }
   // the heads of a call end before the row does: the last row's tail belongs to no head of it
   auto bytes = [&](int w) { return ((rows - 1) * p.ld[w] + static_cast<long long>(Hs[w]) * s.d) * es; };
@@ -151,8 +144,9 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
   p.freqs = cfg->freqs;
   p.mscale = cfg->mscale;
   p.sgn = sgn;
-  // widest access that no section border cuts (interleaved pairs are never cut: borders are even)
-  int V = static_cast<int>(16 / es);
+  // half layout: partners that lie together, up to a whole piece
+  const int V = static_cast<int>(16 / es);
+  int W = 0;
   if (!cfg->interleaved) {
     auto fits = [&](int v) {
       if (cfg->begin % v) return false;
@@ -160,13 +154,11 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
         if (cfg->dims[a] / 2 % v) return false;
       return true;
     };
-    while (V > 1 && !fits(V)) V /= 2;
-    p.n_items = p.rot / 2 / V + (copies ? (s.d - p.rot) / V : 0);
-  } else {
-    p.n_items = s.d / V;
+    for (W = V; W > 1 && !fits(W);) W /= 2;
   }
-  // Long inputs: as many tokens as make one item per thread, whose cosines then serve every head of both
-  // tensors. Short ones: fewer tokens and several threads to an item's heads, so that two blocks come to
+  p.n_items = s.d / V;
+  // Long inputs: as many tokens as make one piece per thread, whose cosines then serve every head of both
+  // tensors. Short ones: fewer tokens and several threads to a piece's heads, so that two blocks come to
   // each SM; when tokens alone are too few for that, the heads are split over blocks too.
   const long long spread = std::max<long long>(1, rows / (2LL * sm_count()));
   p.tt = static_cast<int>(std::min<long long>(spread, std::max(1, kta::ROPE_THREADS / p.n_items)));
@@ -181,11 +173,7 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
   if (gy > 65535) return fail(KTA_ERR_UNSUPPORTED, "too many heads");
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
   cudaStream_t st = as_stream(stream);
-  if (s.dtype == KTA_BF16)
-    return cfg->interleaved ? launch_rope<__nv_bfloat16, false>(p, V, grid, st)
-                            : launch_rope<__nv_bfloat16, true>(p, V, grid, st);
-  return cfg->interleaved ? launch_rope<float, false>(p, V, grid, st)
-                          : launch_rope<float, true>(p, V, grid, st);
+  return s.dtype == KTA_BF16 ? launch_rope<__nv_bfloat16>(p, W, grid, st) : launch_rope<float>(p, W, grid, st);
 }
 
 // ------------------------------------------------------------------------- short convolution

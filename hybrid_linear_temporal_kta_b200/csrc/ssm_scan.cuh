@@ -468,7 +468,6 @@ struct SsmBwdParams {
 // Shared memory of one warp of the local pass: as in the forward, with dout and C beside.
 template <typename T, int NP>
 struct SsmLocalSmem {
-  static constexpr int STAGES = 2;
   struct Raw {
     alignas(16) T u[SSM_TT][SSM_CH];
     alignas(16) T d[SSM_TT][SSM_CH];
@@ -477,7 +476,7 @@ struct SsmLocalSmem {
     alignas(16) T b[SSM_TT][NP];
     alignas(16) T c[SSM_TT][NP];
   };
-  Raw raw[STAGES];
+  Raw raw[2];
   alignas(16) float bc[SSM_TT][2][NP];
   alignas(16) float2 dd[SSM_TT][SSM_CH];   // d, d u
   alignas(16) float dy[SSM_TT][SSM_CH];
@@ -487,7 +486,7 @@ struct SsmLocalSmem {
 template <typename T, int NP>
 __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 4) void ssm_bwd_local_kernel(const SsmBwdParams p) {
   using Smem = SsmLocalSmem<T, NP>;
-  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V, STAGES = Smem::STAGES;
+  constexpr int V = 16 / int(sizeof(T)), CPR = SSM_CH / V;
   extern __shared__ __align__(16) unsigned char ssm_smem[];
   Smem& sm = reinterpret_cast<Smem*>(ssm_smem)[threadIdx.x / 32];
   chain_start();
