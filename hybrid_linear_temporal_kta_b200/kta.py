@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -113,16 +114,16 @@ _SIGS = {
     "kta_stream_load": ([_vp, _vp, _vp], _st),
     "kta_stream_destroy": ([_vp], _st),
     "kta_rope_freqs": ([_i] + [ctypes.c_double] + [_i] + [ctypes.c_double] * 4 + [_vp, _vp], _st),
-    "kta_rope_fwd": ([ctypes.POINTER(Rope), _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
-    "kta_rope_bwd": ([ctypes.POINTER(Rope), _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
-    "kta_short_conv_fwd": ([ctypes.POINTER(ShortConv), _vp, _vp, _vp], _st),
-    "kta_short_conv_bwd_workspace": ([ctypes.POINTER(ShortConv)], ctypes.c_size_t),
-    "kta_short_conv_bwd": ([ctypes.POINTER(ShortConv)] + [_vp] * 7 + [ctypes.c_size_t, _vp], _st),
-    "kta_ssm_scan_fwd_workspace": ([ctypes.POINTER(Ssm)], ctypes.c_size_t),
-    "kta_ssm_scan_fwd": ([ctypes.POINTER(Ssm), _vp, _fp, _vp, ctypes.c_size_t, _vp], _st),
-    "kta_ssm_scan_step": ([ctypes.POINTER(Ssm), _vp, _fp, _vp], _st),
-    "kta_ssm_scan_bwd_workspace": ([ctypes.POINTER(Ssm)], ctypes.c_size_t),
-    "kta_ssm_scan_bwd": ([ctypes.POINTER(Ssm), ctypes.POINTER(SsmGrads), _vp, ctypes.c_size_t, _vp],
+    "kta_rope_fwd": ([_vp, _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
+    "kta_rope_bwd": ([_vp, _vp, _vp, _vp, _vp, Shape, _i, _i, _i, _i, _vp], _st),
+    "kta_short_conv_fwd": ([_vp, _vp, _vp, _vp], _st),
+    "kta_short_conv_bwd_workspace": ([_vp], ctypes.c_size_t),
+    "kta_short_conv_bwd": ([_vp] + [_vp] * 7 + [ctypes.c_size_t, _vp], _st),
+    "kta_ssm_scan_fwd_workspace": ([_vp], ctypes.c_size_t),
+    "kta_ssm_scan_fwd": ([_vp, _vp, _fp, _vp, ctypes.c_size_t, _vp], _st),
+    "kta_ssm_scan_step": ([_vp, _vp, _fp, _vp], _st),
+    "kta_ssm_scan_bwd_workspace": ([_vp], ctypes.c_size_t),
+    "kta_ssm_scan_bwd": ([_vp, _vp, _vp, ctypes.c_size_t, _vp],
                          _st),
     "kta_device_status": ([_vp], _st),
     "kta_selftest_wait_timeout": ([ctypes.c_longlong, _vp], _st),
@@ -571,13 +572,19 @@ class Stream:
             pass
 
 
+# The C structs of these entry points, packed natively (a ctypes.Structure costs twice as long to fill).
+_ROPE = struct.Struct("@7if P i q P")
+_CONV = struct.Struct("@6i 5P")
+_SSM = struct.Struct("@6i 10P")
+_GRADS = struct.Struct("@11P")
+_current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream   # (device index) -> cudaStream_t
 
 
 def _want(t, name, dtype, shape, dev):
-    """Address of t, a contiguous tensor of this dtype and shape on CUDA device dev; None for None."""
+    """Address of t, a contiguous tensor of this dtype and shape on CUDA device dev; 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     _need(t, name, dtype)
@@ -599,12 +606,10 @@ def _io(t, name, dim):
 
 
 def _launch(dev, stream, body, reads):
-    """body(cudaStream_t) on the tensors' device, on its current stream or the one given. What body
+    """body(cudaStream_t) on the tensors' device (made current), on its current stream or the one given. What body
     allocates belongs to that stream (scratch may be reused as soon as the call's work on it is
     done), and tensors of other streams that the call uses are recorded on it."""
     if stream is None:
-        if torch.cuda.current_device() == dev:
-            return body(_raw_stream(dev))
         with torch.cuda.device(dev):
             return body(_raw_stream(dev))
     if stream.device.index != dev:
@@ -643,7 +648,7 @@ def rope_freqs(dims, *, base: float = 10000.0, scaling: str | None = None, facto
     return torch.tensor(out, dtype=torch.float64, device=device), float(m.value)
 
 
-_Int4 = ctypes.c_int * 4
+_PAD = ((), (0, 0, 0), (0, 0), (0,), ())
 
 
 def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, stream):
@@ -657,7 +662,7 @@ def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, s
     if layout != "half" and layout != "interleaved":
         raise ValueError('layout must be "half" or "interleaved"')
     f = _want(freqs, "freqs", torch.float64, (sum(dims) // 2,), dev)
-    per_seq, at = 0, None
+    per_seq = at = 0
     if pos is not None:
         ps = pos.shape
         if ps == (B, N, A) or (A == 1 and ps == (B, N)):
@@ -685,19 +690,21 @@ def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, s
         _want(out[0], "out", ty, shape, dev)
         if k is not None:
             _want(out[1], "out", ty, shape_k, dev)
-    cfg = Rope(A, _Int4(*dims), begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
+    cfg = _ROPE.pack(A, *dims, *_PAD[A], begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
 
     def body(st):
         oq = torch.empty_like(q) if out is None else out[0]
         if k is None:
-            _check(fn(ctypes.byref(cfg), at_q + off, oq.data_ptr() + off, None, None,
+            _check(fn(cfg, at_q + off, oq.data_ptr() + off, None, None,
                       Shape(B, 1, N, d, dt), nq, Hq, 0, 0, st), "kta_rope")
             return oq
         ok = torch.empty_like(k) if out is None else out[1]
-        _check(fn(ctypes.byref(cfg), at_q + off, oq.data_ptr() + off, at_k + off, ok.data_ptr() + off,
+        _check(fn(cfg, at_q + off, oq.data_ptr() + off, at_k + off, ok.data_ptr() + off,
                   Shape(B, 1, N, d, dt), nq, Hq, nk, Hk, st), "kta_rope")
         return oq, ok
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (q, k, freqs, pos) + (out or ()))
 
 
@@ -726,11 +733,11 @@ def _conv_args(x, w, bias, silu, S0, lens, step=False):
     if w.dim() != 2:
         raise ValueError("w must be [D, K]")
     K = w.shape[1]
-    return ShortConv(B, 1 if step else x.shape[1], D, K, dt, bool(silu), at,
-                     _want(w, "w", torch.float32, (D, K), dev),
-                     _want(bias, "bias", torch.float32, (D,), dev),
-                     _want(S0, "S0", ty, (B, K - 1, D), dev),
-                     _want(lens, "lens", torch.int32, (B,), dev)), ty, dev
+    return _CONV.pack(B, 1 if step else x.shape[1], D, K, dt, bool(silu), at,
+                      _want(w, "w", torch.float32, (D, K), dev),
+                      _want(bias, "bias", torch.float32, (D,), dev),
+                      _want(S0, "S0", ty, (B, K - 1, D), dev),
+                      _want(lens, "lens", torch.int32, (B,), dev)), ty, dev, (B, K - 1, D)
 
 
 def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
@@ -740,16 +747,18 @@ def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
     before the first (zeros without). lens [B] int32: rows of each sequence; o is left alone past them
     (fresh buffers are zero there) and the end state is taken there. Returns o (and the last K - 1
     rows)."""
-    c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
+    c, ty, dev, rows = _conv_args(x, w, bias, silu, S0, lens)
     _want(out, "out", ty, x.shape, dev)
 
     def body(st):
         o = _fresh(x, lens) if out is None else out
-        S = torch.empty((c.B, c.K - 1, c.D), device=x.device, dtype=ty) if return_state else None
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), o.data_ptr(),
+        S = torch.empty(rows, device=x.device, dtype=ty) if return_state else None
+        _check(_lib.kta_short_conv_fwd(c, o.data_ptr(),
                                        None if S is None else S.data_ptr(), st), "kta_short_conv_fwd")
         return (o, S) if return_state else o
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (x, w, bias, S0, lens, out))
 
 
@@ -759,15 +768,17 @@ def short_conv_step(x, w, state, bias=None, *, silu: bool = True, state_out=None
     state_out). Returns o [B, D]."""
     if state is None:
         raise ValueError("state must be a tensor")
-    c, ty, dev = _conv_args(x, w, bias, silu, state, None, step=True)
-    end = c.S0 if state_out is None else _want(state_out, "state_out", ty, state.shape, dev)
+    c, ty, dev, rows = _conv_args(x, w, bias, silu, state, None, step=True)
+    end = state.data_ptr() if state_out is None else _want(state_out, "state_out", ty, rows, dev)
     _want(out, "out", ty, x.shape, dev)
 
     def body(st):
         o = torch.empty_like(x) if out is None else out
-        _check(_lib.kta_short_conv_fwd(ctypes.byref(c), o.data_ptr(), end, st), "kta_short_conv_fwd")
+        _check(_lib.kta_short_conv_fwd(c, o.data_ptr(), end, st), "kta_short_conv_fwd")
         return o
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (x, w, bias, state, state_out, out))
 
 
@@ -776,9 +787,9 @@ def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=No
     """Gradients (dx, dw, dbias, dS0) of sum(dout * o) + sum(dS_out * S_out) of short_conv_fwd; dbias
     and dS0 are None without bias and S0. dx is left alone past a sequence's end (a fresh buffer is
     zero there); out = a buffer for dx."""
-    c, ty, dev = _conv_args(x, w, bias, silu, S0, lens)
+    c, ty, dev, rows = _conv_args(x, w, bias, silu, S0, lens)
     g = _want(dout, "dout", ty, x.shape, dev)
-    e = _want(dS_out, "dS_out", ty, (c.B, c.K - 1, c.D), dev)
+    e = _want(dS_out, "dS_out", ty, rows, dev)
     _want(out, "out", ty, x.shape, dev)
 
     def body(st):
@@ -786,14 +797,16 @@ def short_conv_bwd(x, w, dout, bias=None, *, silu: bool = True, S0=None, lens=No
         dw = torch.empty_like(w)
         dbias = None if bias is None else torch.empty_like(bias)
         dS0 = None if S0 is None else torch.empty_like(S0)
-        n = _lib.kta_short_conv_bwd_workspace(ctypes.byref(c))
+        n = _lib.kta_short_conv_bwd_workspace(c)
         ws = _scratch(n, x)
         _check(_lib.kta_short_conv_bwd(
-            ctypes.byref(c), g, e, dx.data_ptr(), dw.data_ptr(),
+            c, g, e, dx.data_ptr(), dw.data_ptr(),
             None if dbias is None else dbias.data_ptr(), None if dS0 is None else dS0.data_ptr(),
             None if ws is None else ws.data_ptr(), n, st), "kta_short_conv_bwd")
         return dx, dw, dbias, dS0
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (x, w, bias, S0, lens, dout, dS_out, out))
 
 
@@ -805,12 +818,13 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, step=False):
     shape, f32 = u.shape, torch.float32
     B, C, N, G = shape[0], shape[-1], A.shape[1], Bm.shape[-2]
     bc = shape[:-1] + (G, N)
-    return Ssm(B, 1 if step else shape[1], C, N, G, code, at, _want(dt, "dt", ty, shape, dev),
-               _want(A, "A", f32, (C, N), dev), _want(Bm, "Bm", ty, bc, dev),
-               _want(Cm, "Cm", ty, bc, dev), _want(D, "D", f32, (C,), dev),
-               _want(z, "z", ty, shape, dev), _want(dt_bias, "dt_bias", f32, (C,), dev),
-               _want(S0, "S0", f32, (B, C, N), dev), _want(lens, "lens", torch.int32, (B,), dev)), \
-        ty, dev
+    states = (B, C, N)
+    return _SSM.pack(B, 1 if step else shape[1], C, N, G, code, at, _want(dt, "dt", ty, shape, dev),
+                     _want(A, "A", f32, (C, N), dev), _want(Bm, "Bm", ty, bc, dev),
+                     _want(Cm, "Cm", ty, bc, dev), _want(D, "D", f32, (C,), dev),
+                     _want(z, "z", ty, shape, dev), _want(dt_bias, "dt_bias", f32, (C,), dev),
+                     _want(S0, "S0", f32, states, dev),
+                     _want(lens, "lens", torch.int32, (B,), dev)), ty, dev, states
 
 
 def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
@@ -820,19 +834,21 @@ def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, len
     [B, L, G, N] like u, group g for channels g D/G ..; D, dt_bias [D] fp32; S0 [B, D, N] fp32. lens
     [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
     end state is taken there. Returns y (and the end state)."""
-    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    c, ty, dev, states = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
     _want(out, "out", ty, u.shape, dev)
 
     def body(st):
         y = _fresh(u, lens) if out is None else out
-        S = torch.empty((c.B, c.D, c.N), device=u.device, dtype=torch.float32) if return_state else None
-        n = _lib.kta_ssm_scan_fwd_workspace(ctypes.byref(c))
+        S = torch.empty(states, device=u.device, dtype=torch.float32) if return_state else None
+        n = _lib.kta_ssm_scan_fwd_workspace(c)
         ws = _scratch(n, u)
-        _check(_lib.kta_ssm_scan_fwd(ctypes.byref(c), y.data_ptr(),
+        _check(_lib.kta_ssm_scan_fwd(c, y.data_ptr(),
                                      None if S is None else S.data_ptr(),
                                      None if ws is None else ws.data_ptr(), n, st), "kta_ssm_scan_fwd")
         return (y, S) if return_state else y
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, out))
 
 
@@ -842,15 +858,17 @@ def ssm_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, stat
     in place (or into state_out). Returns y [B, D]."""
     if state is None:
         raise ValueError("state must be a tensor")
-    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
-    end = c.S0 if state_out is None else _want(state_out, "state_out", torch.float32, state.shape, dev)
+    c, ty, dev, states = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, state, None, step=True)
+    end = state.data_ptr() if state_out is None else _want(state_out, "state_out", torch.float32, states, dev)
     _want(out, "out", ty, u.shape, dev)
 
     def body(st):
         y = torch.empty_like(u) if out is None else out
-        _check(_lib.kta_ssm_scan_step(ctypes.byref(c), y.data_ptr(), end, st), "kta_ssm_scan_step")
+        _check(_lib.kta_ssm_scan_step(c, y.data_ptr(), end, st), "kta_ssm_scan_step")
         return y
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body, (u, dt, A, Bm, Cm, D, z, dt_bias, state, state_out, out))
 
 
@@ -859,9 +877,9 @@ def ssm_scan_bwd(u, dt, A, Bm, Cm, dout, *, D=None, z=None, dt_bias=None, S0=Non
     """Gradients of sum(dout * y) + sum(dS_out * S_out) of ssm_scan_fwd, as a dict: du, ddt, dA, dB,
     dC, and dD, dz, ddt_bias, dS0 (None where the input is). du, ddt, dz, dB, dC are left alone past a
     sequence's end (fresh buffers are zero there); out = a dict of buffers for any of these five."""
-    c, ty, dev = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
+    c, ty, dev, states = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
     do = _want(dout, "dout", ty, u.shape, dev)
-    ds = _want(dS_out, "dS_out", torch.float32, (c.B, c.D, c.N), dev)
+    ds = _want(dS_out, "dS_out", torch.float32, states, dev)
     out = {k: t for k, t in (out or {}).items() if t is not None}
     like = {"du": u, "ddt": dt, "dz": z, "dB": Bm, "dC": Cm}
     for n, t in out.items():
@@ -873,15 +891,17 @@ def ssm_scan_bwd(u, dt, A, Bm, Cm, dout, *, D=None, z=None, dt_bias=None, S0=Non
         g = {n: None if t is None else out[n] if n in out else _fresh(t, lens) for n, t in like.items()}
         for n, t in (("dA", A), ("dD", D), ("ddt_bias", dt_bias), ("dS0", S0)):
             g[n] = None if t is None else torch.empty_like(t)
-        at = {n: None if t is None else t.data_ptr() for n, t in g.items()}
-        n = _lib.kta_ssm_scan_bwd_workspace(ctypes.byref(c))
+        at = {n: 0 if t is None else t.data_ptr() for n, t in g.items()}
+        n = _lib.kta_ssm_scan_bwd_workspace(c)
         ws = _scratch(n, u)
-        grads = SsmGrads(do, ds, at["du"], at["ddt"], at["dA"], at["dB"], at["dC"], at["dD"], at["dz"],
-                         at["ddt_bias"], at["dS0"])
-        _check(_lib.kta_ssm_scan_bwd(ctypes.byref(c), ctypes.byref(grads),
+        grads = _GRADS.pack(do, ds, at["du"], at["ddt"], at["dA"], at["dB"], at["dC"], at["dD"], at["dz"],
+                            at["ddt_bias"], at["dS0"])
+        _check(_lib.kta_ssm_scan_bwd(c, grads,
                                      None if ws is None else ws.data_ptr(), n, st), "kta_ssm_scan_bwd")
         return g
 
+    if stream is None and _current_device() == dev:
+        return body(_raw_stream(dev))
     return _launch(dev, stream, body,
                    (u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, dout, dS_out, *out.values()))
 

@@ -196,6 +196,11 @@ SCAN = [
     (torch.float32, 1, 50, 8, 17, 1, True, False, True, True, [-3]),
     (torch.float32, 2, 9, 264, 3, 1, False, False, False, True, None),
     (torch.float32, 1, 1000, 16, 16, 1, True, True, True, True, None),
+    (torch.bfloat16, 2, 45, 136, 12, 1, True, True, True, True, None),        # rows of 24 bytes
+    (torch.bfloat16, 1, 70, 24, 6, 1, False, True, True, False, None),        # of 12
+    (torch.bfloat16, 2, 40, 16, 24, 1, True, True, True, True, [40, 9]),
+    (torch.float32, 1, 40, 48, 6, 2, True, False, True, True, None),
+    (torch.bfloat16, 5, 100, 520, 16, 5, True, True, True, False, [0, 1, 31, 33, 100]),
 ]
 
 
@@ -317,6 +322,25 @@ def test_scan_extreme_steps(kta):
     assert all(torch.isfinite(t).all() for t in gr.values() if t is not None)
 
 
+@pytest.mark.parametrize("dtype,N", [(torch.bfloat16, 16), (torch.bfloat16, 8), (torch.float32, 16)])
+def test_scan_rows_of_b_and_c_at_any_address(kta, dtype, N):
+    """B and C, and the buffers of their gradients, may begin at any element."""
+    x, kw, _ = scan_case(np.random.default_rng(N), dtype, 1, 90, 24, N, 1, True, True, True, True, None)
+    do = torch.ones_like(x["u"])
+    want_y = kta.ssm_scan_fwd(**x, **kw)
+    want_g = kta.ssm_scan_bwd(**x, dout=do, **kw)
+    for off in (1, 2, 4):
+        def moved(t):
+            buf = torch.full((t.numel() + off,), float("nan"), dtype=t.dtype, device="cuda")
+            buf[off:] = t.reshape(-1)
+            return buf[off:].view(t.shape)
+        y = {**x, "Bm": moved(x["Bm"]), "Cm": moved(x["Cm"])}
+        assert torch.equal(kta.ssm_scan_fwd(**y, **kw), want_y)
+        out = {"dB": moved(x["Bm"]), "dC": moved(x["Cm"])}
+        g = kta.ssm_scan_bwd(**y, dout=do, **kw, out=out)
+        assert g["dB"] is out["dB"] and all(torch.equal(g[n], want_g[n]) for n in g if g[n] is not None)
+
+
 # ---------------------------------------------------------------------------------- calls
 
 def train_step(kta, x, w, bias, scan, kw, do):
@@ -358,6 +382,40 @@ def test_graphs_of_two_calls_replay_at_once(kta):
         torch.cuda.synchronize()
         for got, w in zip(outs, want):
             assert all(torch.equal(x, y) for x, y in zip(got, w))
+
+
+def test_rollout_replayed_as_a_graph(kta):
+    """Steps in place inside a graph: each replay moves rows and state on by one token."""
+    x, kw, _ = scan_case(np.random.default_rng(8), torch.bfloat16, 3, 12, 40, 16, 1, True, True, True, True, None)
+    w, b = torch.randn(40, 4, device="cuda"), torch.randn(40, device="cuda")
+    rows, state = torch.randn(3, 3, 40, device="cuda").bfloat16(), kw.pop("S0")
+    tok = {n: t[:, 0].contiguous() for n, t in {**x, "z": kw["z"]}.items() if n != "A"}
+
+    def one(rows, state):
+        u = kta.short_conv_step(tok["u"], w, rows, b)
+        return kta.ssm_scan_step(u, tok["dt"], x["A"], tok["Bm"], tok["Cm"], state, D=kw["D"], z=tok["z"],
+                                 dt_bias=kw["dt_bias"])
+
+    def put(t):
+        for n in tok:
+            tok[n].copy_((x[n] if n in x else kw[n])[:, t])
+
+    mine = rows.clone(), state.clone()
+    want = []
+    for t in range(12):
+        put(t)
+        want.append(one(*mine))
+    one(rows.clone(), state.clone())
+    g = torch.cuda.CUDAGraph()
+    r2, s2 = rows.clone(), state.clone()
+    with torch.cuda.graph(g):
+        y = one(rows, state)
+    rows.copy_(r2), state.copy_(s2)
+    for t in range(12):
+        put(t)
+        g.replay()
+        assert torch.equal(y, want[t])
+    assert torch.equal(rows, mine[0]) and torch.equal(state, mine[1])
 
 
 def test_calls_on_two_streams_at_once(kta):
