@@ -176,15 +176,23 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
   return s.dtype == KTA_BF16 ? launch_rope<__nv_bfloat16>(p, W, grid, st) : launch_rope<float>(p, W, grid, st);
 }
 
+// Tokens are counted in 32 bits; a run or segment, and the rows fetched ahead, may end behind the last one.
+kta_status check_rows(int B, int L) {
+  if (static_cast<long long>(B) * L >= (1LL << 31) - (1 << 16))
+    return fail(KTA_ERR_UNSUPPORTED, "B*L must be < 2^31 - 2^16");
+  return KTA_OK;
+}
+
 // ------------------------------------------------------------------------- short convolution
 
 kta_status check_conv(const kta_short_conv* c) {
+  kta_status r;
   if (!c) return fail(KTA_ERR_INVALID_ARG, "null convolution description");
   if (c->B < 1 || c->L < 1 || c->D < 1) return fail(KTA_ERR_INVALID_ARG, "B, L, D must be >= 1");
   if (c->dtype != KTA_BF16 && c->dtype != KTA_F32) return fail(KTA_ERR_INVALID_ARG, "bad dtype");
   if (c->K < 2 || c->K > 4) return fail(KTA_ERR_UNSUPPORTED, "K must be 2, 3 or 4 (got %d)", c->K);
   if (c->D % 8) return fail(KTA_ERR_ALIGNMENT, "D must be a multiple of 8 (16-byte rows)");
-  if (static_cast<long long>(c->B) * c->L >= (1LL << 31)) return fail(KTA_ERR_UNSUPPORTED, "B*L must be < 2^31");
+  if ((r = check_rows(c->B, c->L))) return r;
   if (c->D >= (1 << 28)) return fail(KTA_ERR_UNSUPPORTED, "D must be < 2^28");
   if (reinterpret_cast<uintptr_t>(c->lens) & 3) return fail(KTA_ERR_ALIGNMENT, "lens must be 4-byte aligned");
   return KTA_OK;
@@ -280,6 +288,7 @@ kta_status conv_fwd_common(const kta_short_conv* c, void* o, void* S_out, void* 
 // ------------------------------------------------------------------------- state-space scan
 
 kta_status check_ssm(const kta_ssm* c) {
+  kta_status r;
   if (!c) return fail(KTA_ERR_INVALID_ARG, "null scan description");
   if (c->B < 1 || c->L < 1 || c->D < 1 || c->N < 1 || c->G < 1)
     return fail(KTA_ERR_INVALID_ARG, "B, L, D, N, G must be >= 1");
@@ -289,7 +298,7 @@ kta_status check_ssm(const kta_ssm* c) {
   if (c->D % c->G) return fail(KTA_ERR_INVALID_ARG, "G must divide D");
   if (c->D / c->G % 8)
     return fail(KTA_ERR_ALIGNMENT, "the channels of a group must be a multiple of 8 (16-byte rows)");
-  if (static_cast<long long>(c->B) * c->L >= (1LL << 31)) return fail(KTA_ERR_UNSUPPORTED, "B*L must be < 2^31");
+  if ((r = check_rows(c->B, c->L))) return r;
   if (c->D >= (1 << 26)) return fail(KTA_ERR_UNSUPPORTED, "D must be < 2^26");
   if (reinterpret_cast<uintptr_t>(c->lens) & 3) return fail(KTA_ERR_ALIGNMENT, "lens must be 4-byte aligned");
   return KTA_OK;

@@ -318,6 +318,11 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
 // states that enter them. Loads of SSM_CARRY_UNROLL segments are in flight at once.
 constexpr int SSM_CARRY_UNROLL = 8;
 
+// 2^x h + v: a state still at zero stays there where a segment's growth (A > 0) overflows.
+__device__ __forceinline__ float ssm_carry(float x, float h, float v) {
+  return h == 0.f ? v : fmaf(ex2_approx(x), h, v);
+}
+
 __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, int NP) {
   const long long per = static_cast<long long>(p.D) * NP;
   const long long gid = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -342,7 +347,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, i
     for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
       if (s0 + i < p.nseg) {
         hs[(s0 + i) * per] = h;
-        if (s0 + i < p.nseg - 1) h = fmaf(ex2_approx(d[i] * A2), h, v[i]);
+        if (s0 + i < p.nseg - 1) h = ssm_carry(d[i] * A2, h, v[i]);
       }
   }
 }
@@ -618,7 +623,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p
     for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
       if (s0 + i < S) {
         vs[step * (s0 + i) * per] = h;
-        h = fmaf(ex2_approx(d[i] * A2), h, v[i]);
+        h = ssm_carry(d[i] * A2, h, v[i]);
       }
   }
   if (back && on && p.dS0) p.dS0[eb] = h;

@@ -690,7 +690,10 @@ def _rope(fn, q, k, freqs, dims, begin, layout, mscale, pos, pos0, heads, out, s
         _want(out[0], "out", ty, shape, dev)
         if k is not None:
             _want(out[1], "out", ty, shape_k, dev)
-    cfg = _ROPE.pack(A, *dims, *_PAD[A], begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
+    try:
+        cfg = _ROPE.pack(A, *dims, *_PAD[A], begin, layout == "interleaved", mscale, at, per_seq, pos0, f)
+    except struct.error as e:
+        raise ValueError(f"dims, begin or pos0: {e}") from None
 
     def body(st):
         oq = torch.empty_like(q) if out is None else out[0]
@@ -916,6 +919,9 @@ def selftest_wait_timeout(budget_cycles: int, stream=None):
            "kta_selftest_wait_timeout")
 
 
+_TRACE_NAMES = 64   # more than the library has kernel names
+
+
 class trace:
     """Context manager: per-kernel launch counts and device milliseconds of every library kernel
     launched inside the block (CUDA events on each launch's own stream)."""
@@ -926,7 +932,7 @@ class trace:
         return self
 
     def __exit__(self, *exc):
-        cap = 32
+        cap = _TRACE_NAMES
         n = _i()
         names = (ctypes.c_char_p * cap)()
         launches = (_i * cap)()

@@ -432,7 +432,7 @@ kta_status kta_rope_freqs(int dims, double base, int scaling, double factor, dou
  * paper-read's GLA paragraph names as the branch's basis, has one; the pages do not show it):
  *     pre_t = bias + sum_{j<K} w_j x_{t-K+1+j},   o_t = silu(pre_t) (silu = 1) or pre_t.
  *  - x, o: [B][L][D] (dtype); w: [D][K] fp32; bias: [D] fp32 or NULL. K in {2, 3, 4}; D % 8 == 0;
- *    every pointer 16-byte aligned.
+ *    B*L < 2^31 - 2^16; every pointer 16-byte aligned.
  *  - S0: [B][K-1][D] (dtype), the K - 1 rows before the first (oldest first), or NULL = zeros.
  *    S_out: the last K - 1 rows of [S0; x], or NULL. S_out = S0 updates the state in place; with
  *    L = 1 this is the step of a rollout.
@@ -468,9 +468,10 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
  * channel c of group g and state n < N:
  *     h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,   y_t = (sum_n C_t h_t + D_skip u_t) silu(z_t).
  *  - u, dt, z, y: [B][L][D] (dtype); Bm, Cm: [B][L][G][N] (dtype), group g = c / (D / G);
- *    A: [D][N] fp32 (negative for a decaying state; any finite value is taken); D_skip, dt_bias: [D]
- *    fp32 or NULL (= 0); z NULL = no gate. 1 <= N <= 32; G divides D; (D / G) % 8 == 0; every
- *    pointer 16-byte aligned, but Bm, Cm and their gradients by their element alone.
+ *    A: [D][N] fp32, negative for a decaying state (a positive one grows it: the backward pass needs
+ *    exp(A sum d) over 32 tokens within fp32's range); D_skip, dt_bias: [D] fp32 or NULL (= 0);
+ *    z NULL = no gate. 1 <= N <= 32; G divides D; (D / G) % 8 == 0; B*L < 2^31 - 2^16; every pointer
+ *    16-byte aligned, but Bm, Cm and their gradients by their element alone.
  *  - S0, S_out: [B][D][N] fp32, the state before the first and after the last token; NULL = zero / not
  *    wanted. States and sums are fp32; y is rounded once.
  *  - lens: as in kta_short_conv.

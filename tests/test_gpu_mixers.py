@@ -322,6 +322,29 @@ def test_scan_extreme_steps(kta):
     assert all(torch.isfinite(t).all() for t in gr.values() if t is not None)
 
 
+def test_scan_of_growing_states_that_are_still_zero(kta):
+    """A > 0 whose growth over a segment overflows: a state that no input has reached stays zero, and the
+    last tokens come out as in a call of their own."""
+    L, D, N = 512, 8, 16
+    g = torch.Generator("cuda").manual_seed(3)
+    r = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    u, Bm, Cm = r(1, L, D), r(1, L, 1, N), r(1, L, 1, N)
+    u[:, :-2] = 0
+    dt, A = torch.full_like(u, 3.5), torch.ones(D, N, device="cuda")   # exp(32 softplus(3.5)) > 2^128
+    y, S = kta.ssm_scan_fwd(u, dt, A, Bm, Cm, return_state=True)
+    last = [t[:, -2:].contiguous() for t in (u, dt, Bm, Cm)]
+    y2, S2 = kta.ssm_scan_fwd(*last[:2], A, *last[2:], return_state=True)
+    assert (y[:, :-2] == 0).all() and torch.equal(y[:, -2:], y2) and torch.equal(S, S2)
+    assert torch.isfinite(S).all()
+
+
+def test_rope_refuses_numbers_out_of_range(kta):
+    q, f = torch.zeros(1, 4, 2, 64, device="cuda"), torch.ones(16, device="cuda", dtype=torch.float64)
+    for kw in (dict(pos0=1 << 64), dict(pos0=0.5), dict(begin=1 << 40), dict(dims=(32.0,))):
+        with pytest.raises(ValueError):
+            kta.rope_fwd(q, freqs=f, **{"dims": 32, **kw})
+
+
 @pytest.mark.parametrize("dtype,N", [(torch.bfloat16, 16), (torch.bfloat16, 8), (torch.float32, 16)])
 def test_scan_rows_of_b_and_c_at_any_address(kta, dtype, N):
     """B and C, and the buffers of their gradients, may begin at any element."""

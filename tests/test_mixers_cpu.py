@@ -205,3 +205,23 @@ def test_binding_refuses_what_is_not_on_a_gpu(kta):
         kta.ssm_scan_fwd(x, x, torch.zeros(16, 16), torch.zeros(2, 9, 1, 16), torch.zeros(2, 9, 1, 16))
     with pytest.raises(ValueError):
         kta.rope_freqs(32, scaling="other", device="cpu")
+
+
+def test_token_counts_leave_room_for_what_ends_behind_the_last_row(kta):
+    """Tokens are counted in 32 bits, and the ends of runs and segments are rounded up."""
+    for L in ((1 << 31) - 1, (1 << 31) - (1 << 16)):
+        c, s, g = conv(kta, B=1, L=L), ssm(kta, B=1, L=L), grads(kta)
+        assert kta.raw_call("kta_short_conv_fwd", ctypes.byref(c), at(8), at(9), ST) == UNSUPPORTED
+        assert kta._lib.kta_short_conv_bwd_workspace(ctypes.byref(c)) == 0
+        assert kta.raw_call("kta_ssm_scan_fwd", ctypes.byref(s), at(10), at(11), at(12), 1 << 40, ST) == UNSUPPORTED
+        assert kta.raw_call("kta_ssm_scan_bwd", ctypes.byref(s), ctypes.byref(g), at(12), 1 << 60, ST) == UNSUPPORTED
+    assert kta._lib.kta_ssm_scan_bwd_workspace(ctypes.byref(ssm(kta, B=1, L=(1 << 31) - (1 << 16) - 1))) > 0
+
+
+def test_trace_has_room_for_every_kernel_name(kta):
+    import pathlib
+    import re
+    csrc = pathlib.Path(kta.__file__).parent / "csrc"
+    names = {n for f in csrc.glob("*.cu*") for line in f.read_text().splitlines() if "TraceScope" in line
+             for n in re.findall(r'"(\w+)"', line)}
+    assert 30 < len(names) <= kta._TRACE_NAMES
