@@ -17,12 +17,13 @@ namespace kta {
 constexpr int SC_THREADS = 128;
 constexpr int SC_V = 4;             // channels per thread
 constexpr int SC_UNROLL = 4;        // rows loaded before the first is used (forward)
-constexpr int SC_RUN = 64;          // tokens of a run, at most
+constexpr int SC_RUN = 64;          // tokens of a run, at most (backward: of one that need not fill the card evenly)
 constexpr int SC_MIN_RUN = 8;       // and at least: more than K - 1
 constexpr int SC_RING = 4;          // rows in flight per thread (backward)
 constexpr int SC_BWD_UNROLL = 8;    // rows between two register renamings of the windows (backward)
 constexpr int SC_BWD_X = 32;        // pieces of the channels per block (backward)
 constexpr int SC_BWD_Y = 4;         // runs per block (backward)
+constexpr int SC_BWD_BLOCKS = 4;    // blocks on an SM (backward)
 
 struct ConvParams {
   const void *x, *S0, *dout, *dS_out;
@@ -151,7 +152,7 @@ __device__ __forceinline__ uint64_t conv_pair(const VecPack<float, 4>& v, int i)
 // a ring of the thread's own pieces in shared memory, SC_RING ahead, so nothing waits for a load but the
 // first; arithmetic runs on packed pairs of channels.
 template <typename T, int K, bool SILU>
-__global__ __launch_bounds__(SC_BWD_X* SC_BWD_Y, 4) void short_conv_bwd_kernel(const ConvParams p) {
+__global__ __launch_bounds__(SC_BWD_X* SC_BWD_Y, SC_BWD_BLOCKS) void short_conv_bwd_kernel(const ConvParams p) {
   constexpr int V = SC_V, P = V / 2;
   __shared__ typename VecPack<T, V>::Raw ring[SC_RING][2][SC_BWD_X * SC_BWD_Y];
   __shared__ __align__(16) float red[SC_BWD_Y][K + 1][SC_BWD_X * V + 4];
