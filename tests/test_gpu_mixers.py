@@ -162,6 +162,19 @@ def test_short_conv_backward_parity(kta, dtype, B, L, D, K, silu, bias, S0, lens
         assert all(a is None or torch.equal(a, c) for a, c in zip(got, again))
 
 
+def test_short_conv_backward_of_runs_that_fill_the_card(kta):
+    """Enough rows and channels that the runs are stretched (100 tokens here on 148 SMs), with one sequence
+    that ends inside a run."""
+    x, w, b, s, n, seen = conv_case(np.random.default_rng(11), torch.bfloat16, 2, 3600, 4096, 4, True, True, [3600, 1551])
+    do = gpu(np.random.default_rng(12).standard_normal(x.shape), torch.bfloat16)
+    do[1, 1551:] = float("nan")
+    got = kta.short_conv_bwd(x, w, do, b, S0=s, lens=n)
+    want = mixers.short_conv(np.nan_to_num(host(x)), host(w), host(b), silu=True, S0=host(s), lens=seen,
+                             dout=np.nan_to_num(host(do)), bounds=True)
+    for name, g in zip(("dx", "dw", "dbias", "dS0"), got):
+        check(name, g, want[name])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("K", [2, 3, 4])
 def test_short_conv_rollout_is_the_whole_sequence(kta, dtype, K):
