@@ -208,16 +208,29 @@ int conv_run(const kta_short_conv* c) {
   return run;
 }
 
-// Backward: when runs of SC_RUN would fill the card's blocks more than once, runs are stretched so that they
-// fill it a whole number of times (2 x 12,000 x 2,048: 98 us with runs of 64, 92 stretched; 2 x 8,191: level).
+// Backward: runs are stretched towards a whole number of turns of the card where that shortens the path of its
+// busiest SM. A turn of k blocks there takes (run + K - 1) (2 + 4 k) units: a row costs a warp half as
+// much again as its share of the SM's issue. (Fits 120 measured plans to 2 %.) us with runs of 64 / of the
+// stretched length, turns of the card as the stretched blocks fill it:
+//   stretched: 2 x 3,600 x 4,096  67.0 / 58.3 (0.97), 2 x 12,000 x 2,048  97.1 / 91.0 (2.00),
+//     8 x 1,759 x 7,936  197.5 / 187.7 (4.19);
+//   kept: 8 x 768 x 5,120  66.6 / 80.8 (0.54), 24 x 512 x 4,096  97.2 / 103.3 (1.30),
+//     8 x 4,096 x 2,048  119.9 / 126.0 (2.81).
 int conv_bwd_run(const kta_short_conv* c) {
   const int run = conv_run(c);
   const long long per = static_cast<long long>(c->B) * ((c->D / kta::SC_V + kta::SC_BWD_X - 1) / kta::SC_BWD_X);
-  const long long slots = static_cast<long long>(kta::SC_BWD_BLOCKS) * sm_count();
-  const long long groups = (c->L + run * kta::SC_BWD_Y - 1) / (run * kta::SC_BWD_Y), waves = per * groups / slots;
-  const long long fit = waves * slots / per;               // blocks of runs per sequence
-  if (run < kta::SC_RUN || fit < 1 || fit >= groups) return run;
-  return static_cast<int>((c->L + fit * kta::SC_BWD_Y - 1) / (fit * kta::SC_BWD_Y));
+  const long long sms = sm_count(), slots = kta::SC_BWD_BLOCKS * sms;
+  auto blocks = [&](int r) {                               // of the grid, as the launch counts them
+    return per * (((c->L + r - 1) / r + kta::SC_BWD_Y - 1) / kta::SC_BWD_Y);
+  };
+  auto path = [&](int r) {
+    const long long n = blocks(r), rest = (n % slots + sms - 1) / sms;
+    return (r + c->K - 1) * (n / slots * (2 + 4 * kta::SC_BWD_BLOCKS) + (rest ? 2 + 4 * rest : 0));
+  };
+  const long long fit = blocks(run) / slots * slots / per;       // blocks of runs per sequence
+  if (run < kta::SC_RUN || fit < 1) return run;
+  const int longer = static_cast<int>((c->L + fit * kta::SC_BWD_Y - 1) / (fit * kta::SC_BWD_Y));
+  return longer > run && path(longer) < path(run) ? longer : run;
 }
 
 kta::ConvParams conv_params(const kta_short_conv* c, bool bwd) {

@@ -17,7 +17,7 @@ namespace kta {
 constexpr int SC_THREADS = 128;
 constexpr int SC_V = 4;             // channels per thread
 constexpr int SC_UNROLL = 4;        // rows loaded before the first is used (forward)
-constexpr int SC_RUN = 64;          // tokens of a run, at most (backward: of one that need not fill the card evenly)
+constexpr int SC_RUN = 64;          // tokens of a run, at most (backward: of one that is not stretched)
 constexpr int SC_MIN_RUN = 8;       // and at least: more than K - 1
 constexpr int SC_RING = 4;          // rows in flight per thread (backward)
 constexpr int SC_BWD_UNROLL = 8;    // rows between two register renamings of the windows (backward)

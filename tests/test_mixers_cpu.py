@@ -225,3 +225,15 @@ def test_trace_has_room_for_every_kernel_name(kta):
     names = {n for f in csrc.glob("*.cu*") for line in f.read_text().splitlines() if "TraceScope" in line
              for n in re.findall(r'"(\w+)"', line)}
     assert 30 < len(names) <= kta._TRACE_NAMES
+
+
+@pytest.mark.parametrize("B,L,D,longer", [
+    (2, 8191, 2048, True), (2, 3600, 4096, True), (2, 12000, 2048, True), (16, 1085, 3456, True), (8, 1759, 7936, True),
+    (1, 65536, 2048, True), (8, 768, 5120, False), (16, 768, 2560, False), (24, 512, 4096, False), (8, 4096, 2048, False),
+    (24, 5051, 1472, False), (16, 2048, 4096, False), (1, 64, 2048, False)])
+def test_conv_backward_stretches_runs_where_measured_faster(kta, B, L, D, longer):
+    """The workspace tells the blocks of a call (4 runs each) on 148 SMs: runs of 64 tokens where longer ones
+    were measured to take as long or longer, fewer blocks where they were faster."""
+    n = kta._lib.kta_short_conv_bwd_workspace(ctypes.byref(conv(kta, B=B, L=L, D=D)))
+    blocks, of64 = n // (5 * D * 4), B * -(-L // 256)
+    assert blocks < of64 if longer else blocks >= of64
