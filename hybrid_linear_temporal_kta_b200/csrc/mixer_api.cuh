@@ -128,6 +128,11 @@ kta_status rope_common(const kta_rope* cfg, const void* x, void* o, const void* 
     const long long na = static_cast<long long>(Hs[wa]) * s.d * es, nb = static_cast<long long>(Hs[wb]) * s.d * es;
     return !(off >= na && off + nb <= row);
   };
+  // angles are read again while heads are written
+  const size_t npos = 8 * static_cast<size_t>(cfg->pos_per_seq ? rows : N) * cfg->n_axes, nfreq = 4 * static_cast<size_t>(rot);
+  for (int w = 0; w < 2; ++w)
+    if (overlaps(os[w], bytes(w), cfg->pos, npos) || overlaps(os[w], bytes(w), cfg->freqs, nfreq))
+      return fail(KTA_ERR_INVALID_ARG, "an output overlaps pos or freqs");
   if ((o != x && clash(o, 0, x, 0)) ||
       (two && ((o2 != x2 && clash(o2, 1, x2, 1)) || clash(o, 0, x2, 1) || clash(o2, 1, x, 0) ||
                clash(o, 0, o2, 1))))
@@ -290,9 +295,10 @@ kta_status conv_fwd_common(const kta_short_conv* c, void* o, void* S_out, void* 
                     {c->w, nw, false, true, "w"},
                     {c->bias, static_cast<size_t>(c->D) * 4, false, false, "bias"},
                     {in_place ? nullptr : c->S0, ns, false, false, "S0"},
+                    {c->lens, static_cast<size_t>(c->B) * 4, false, false, "lens", 4},
                     {o, n, true, true, "o"},
                     {S_out, ns, true, false, "S_out"}};
-  if ((r = check_spans(v, 6))) return r;
+  if ((r = check_spans(v, 7))) return r;
   kta::ConvParams p = conv_params(c, false);
   p.o = o;
   p.S_out = S_out;
@@ -329,7 +335,7 @@ kta_status check_ssm(const kta_ssm* c) {
   return KTA_OK;
 }
 
-constexpr int kSsmInputs = 9;
+constexpr int kSsmInputs = 10;
 
 void ssm_inputs(const kta_ssm* c, Span* v) {
   const size_t es = elem_size(c->dtype), rows = static_cast<size_t>(c->B) * c->L;
@@ -343,6 +349,7 @@ void ssm_inputs(const kta_ssm* c, Span* v) {
   v[6] = {c->z, n, false, false, "z"};
   v[7] = {c->dt_bias, d4, false, false, "dt_bias"};
   v[8] = {c->S0, d4 * c->N * c->B, false, false, "S0"};
+  v[9] = {c->lens, static_cast<size_t>(c->B) * 4, false, false, "lens", 4};
 }
 
 kta::SsmParams ssm_params(const kta_ssm* c) {
@@ -617,8 +624,9 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
                     {dout, n, false, true, "dout"},    {dS_out, ns, false, false, "dS_out"},
                     {dx, n, true, true, "dx"},         {dw, nw, true, true, "dw"},
                     {dbias, nb, true, false, "dbias"}, {dS0, ns, true, false, "dS0"},
+                    {c->lens, static_cast<size_t>(c->B) * 4, false, false, "lens", 4},
                     {ws, need, true, false, "the workspace"}};
-  if ((r = check_spans(v, 11))) return r;
+  if ((r = check_spans(v, 12))) return r;
   kta::ConvParams p = conv_params(c, true);
   p.dout = dout;
   p.dS_out = dS_out;

@@ -237,3 +237,30 @@ def test_conv_backward_stretches_runs_where_measured_faster(kta, B, L, D, longer
     n = kta._lib.kta_short_conv_bwd_workspace(ctypes.byref(conv(kta, B=B, L=L, D=D)))
     blocks, of64 = n // (5 * D * 4), B * -(-L // 256)
     assert blocks < of64 if longer else blocks >= of64
+
+
+def test_outputs_over_lengths_positions_or_frequencies_are_refused(kta):
+    """They are read again while outputs are written."""
+    big, n8 = 1 << 33, 2 * 9 * 16 * 2                       # bytes of x, o, u, y
+    c = conv(kta, lens=at(9, n8 - 4))                       # the last element of an output at at(9)
+    fwd = lambda c, o, S: kta.raw_call("kta_short_conv_fwd", ctypes.byref(c), o, S, ST)  # noqa: E731
+    assert fwd(c, at(9), None) == INVALID and fwd(c, at(8), at(9, n8 - 16)) == INVALID
+    c.lens = at(9, 4)
+    for k in range(5):                                      # dx, dw, dbias, dS0, the workspace
+        outs = [at(9) if i == k else at(20 + i) for i in range(5)]
+        assert kta.raw_call("kta_short_conv_bwd", ctypes.byref(c), at(8), None, *outs, big, ST) == INVALID, k
+    s = ssm(kta, lens=at(9, 4))
+    assert kta.raw_call("kta_ssm_scan_fwd", ctypes.byref(s), at(9), at(11), at(12), big, ST) == INVALID
+    assert kta.raw_call("kta_ssm_scan_fwd", ctypes.byref(s), at(10), at(9), at(12), big, ST) == INVALID
+    many = ssm(kta, B=1, L=4096, lens=at(9, 4))             # cut into segments: it has a workspace
+    assert kta._lib.kta_ssm_scan_fwd_workspace(ctypes.byref(many)) > 0
+    assert kta.raw_call("kta_ssm_scan_fwd", ctypes.byref(many), at(10), at(11), at(9), big, ST) == INVALID
+    for name in ("du", "ddt", "dA", "dB", "dC", "dD_skip", "dz", "ddt_bias", "dS0"):
+        g = grads(kta, **{name: at(9)})
+        assert kta.raw_call("kta_ssm_scan_bwd", ctypes.byref(s), ctypes.byref(g), at(12), big, ST) == INVALID, name
+    assert kta.raw_call("kta_ssm_scan_bwd", ctypes.byref(s), ctypes.byref(grads(kta)), at(9), big, ST) == INVALID
+    row = 2 * 16 * 2 * 64 * 2                               # bytes of o: 32 tokens of 2 heads of 64
+    for kw in (dict(pos=at(1, row - 8)), dict(freqs=at(1, row - 8)), dict(o=at(5, 8 * 32 - 16)), dict(o=at(6, 8 * 16 - 16)),
+               dict(x2=at(2), o2=at(3), H2=2, ld2=2, pos=at(3, 64)), dict(x2=at(2), o2=at(3), H2=2, ld2=2, freqs=at(3, 64)),
+               dict(o=at(0), pos=at(0, 64))):
+        assert rope_call(kta, **kw) == INVALID, kw
