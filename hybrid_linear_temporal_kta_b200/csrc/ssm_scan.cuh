@@ -318,9 +318,13 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
 // states that enter them. Loads of SSM_CARRY_UNROLL segments are in flight at once.
 constexpr int SSM_CARRY_UNROLL = 8;
 
-// 2^x h + v: a state still at zero stays there where a segment's growth (A > 0) overflows.
+// 2^x h + v. Where a segment's growth alone overflows (A > 0) it is applied in two halves: 2^x h is then formed
+// whenever h and it are normal numbers, and a state still at zero stays there.
 __device__ __forceinline__ float ssm_carry(float x, float h, float v) {
-  return h == 0.f ? v : fmaf(ex2_approx(x), h, v);
+  if (h == 0.f) return v;
+  if (x < 128.f) return fmaf(ex2_approx(x), h, v);
+  const float half = ex2_approx(0.5f * x);
+  return fmaf(half, half * h, v);
 }
 
 __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, int NP) {

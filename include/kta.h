@@ -468,8 +468,9 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
  * channel c of group g and state n < N:
  *     h_t = exp(d_t A) h_{t-1} + d_t u_t B_t,   y_t = (sum_n C_t h_t + D_skip u_t) silu(z_t).
  *  - u, dt, z, y: [B][L][D] (dtype); Bm, Cm: [B][L][G][N] (dtype), group g = c / (D / G);
- *    A: [D][N] fp32, negative for a decaying state (a positive one grows it: the backward pass needs
- *    exp(A sum d) over 32 tokens within fp32's range); D_skip, dt_bias: [D] fp32 or NULL (= 0);
+ *    A: [D][N] fp32, negative for a decaying state (a positive one grows it: the forward pass needs
+ *    the states themselves within fp32's normal range, the backward pass exp(A sum d) over 32 tokens too);
+ *    D_skip, dt_bias: [D] fp32 or NULL (= 0);
  *    z NULL = no gate. 1 <= N <= 32; G divides D; (D / G) % 8 == 0; B*L < 2^31 - 2^16; every pointer
  *    16-byte aligned, but Bm, Cm and their gradients by their element alone.
  *  - S0, S_out: [B][D][N] fp32, the state before the first and after the last token; NULL = zero / not

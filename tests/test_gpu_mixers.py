@@ -351,6 +351,30 @@ def test_scan_of_growing_states_that_are_still_zero(kta):
     assert torch.isfinite(S).all()
 
 
+@pytest.mark.parametrize("scale", [1e-30, -1e-20, 2.0 ** -126])
+def test_scan_of_small_states_that_grow(kta, scale):
+    """A > 0: growth over one segment that overflows alone, while the state that it acts on stays finite; cut
+    into segments or not, the state is the formula's."""
+    L, D, N = 512, 8, 16
+    r = np.random.default_rng(4)
+    dt = np.full((1, L, D), -200.0)
+    dt[:, 64:96] = np.log(np.expm1((90 if abs(scale) > 1e-25 else 96) / 32))        # e^90, e^96 over the 32 tokens
+    x = {"u": torch.zeros(1, L, D, device="cuda"), "dt": gpu(dt), "A": torch.ones(D, N, device="cuda"),
+         "Bm": gpu(r.standard_normal((1, L, 1, N))), "Cm": gpu(r.standard_normal((1, L, 1, N)))}
+    kw = {"S0": gpu(scale * r.uniform(1, 2, (1, D, N)))}
+    y, S = kta.ssm_scan_fwd(**x, **kw, return_state=True)
+    want = scan_oracle(x, kw, None)
+    check("S_out", S, want["S_out"])
+    check("y", y, want["y"])
+    state, rows = kw["S0"], []
+    for a in range(0, L, 32):                               # one segment each
+        piece = {n: t if n == "A" else t[:, a:a + 32].contiguous() for n, t in x.items()}
+        o, state = kta.ssm_scan_fwd(**piece, S0=state, return_state=True)
+        rows.append(o)
+    check("S in pieces", state, want["S_out"])
+    check("y in pieces", torch.cat(rows, 1), want["y"])
+
+
 def test_rope_refuses_numbers_out_of_range(kta):
     q, f = torch.zeros(1, 4, 2, 64, device="cuda"), torch.ones(16, device="cuda", dtype=torch.float64)
     for kw in (dict(pos0=1 << 64), dict(pos0=0.5), dict(begin=1 << 40), dict(dims=(32.0,))):
