@@ -6,6 +6,8 @@
 // Bound by the exponential unit: one exponential per (token, channel, state), a warp's 32 in 8 cycles
 // of its scheduler, against 8 bytes per (token, channel) in bf16.
 #pragma once
+#include <float.h>
+
 #include "mixer_common.cuh"
 
 namespace kta {
@@ -73,6 +75,11 @@ __device__ __forceinline__ void ssm_store_states(float* row, int q, int N, const
       if (q * NS + i < N) row[q * NS + i] = f[i];
   }
 }
+
+// log2(e) A, kept finite: an infinite A then forgets (or grows) at every step d > 0 and leaves the state alone
+// where d = 0, as in the rows that pad a tile.
+__device__ __forceinline__ float ssm_finite(float x) { return fabsf(x) > FLT_MAX ? copysignf(FLT_MAX, x) : x; }
+__device__ __forceinline__ float ssm_log2(float A) { return ssm_finite(A * 1.4426950408889634f); }
 
 // Starts the copies of TT rows of B (and of C, if C) to their raw tile.
 template <typename T, int NP, int TT, bool C, int BYTES>
@@ -208,8 +215,8 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
   const float* Arow = p.A + static_cast<long long>(c) * p.N;
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) {
-    A2[i].x = 2 * i < p.N ? Arow[2 * i] * 1.4426950408889634f : 0.f;
-    A2[i].y = 2 * i + 1 < p.N ? Arow[2 * i + 1] * 1.4426950408889634f : 0.f;
+    A2[i].x = 2 * i < p.N ? ssm_log2(Arow[2 * i]) : 0.f;
+    A2[i].y = 2 * i + 1 < p.N ? ssm_log2(Arow[2 * i + 1]) : 0.f;
     h[i] = make_float2(0.f, 0.f);
   }
   if (OUT && p.nseg > 1) {                               // entering states, left by ssm_fwd_carry
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, i
   const int n = static_cast<int>(gid % per / p.D), c = static_cast<int>(gid % p.D);
   const long long e = static_cast<long long>(c) * p.N + n;
   const bool on = n < p.N;
-  const float A2 = on ? p.A[e] * 1.4426950408889634f : 0.f;
+  const float A2 = on ? ssm_log2(p.A[e]) : 0.f;
   float h = on && p.S0 ? p.S0[static_cast<long long>(b) * p.D * p.N + e] : 0.f;
   float* hs = p.seg_h + (static_cast<long long>(b) * p.nseg * NP + n) * p.D + c;
   const float* ds = p.seg_d + static_cast<long long>(b) * p.nseg * p.D + c;
@@ -406,7 +413,7 @@ __global__ __launch_bounds__(SSM_THREADS) void ssm_step_kernel(const SsmParams p
   float A2[NS];
   ssm_load_states<NS>(p.A + static_cast<long long>(c) * p.N, q, p.N, A2);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) A2[i] *= 1.4426950408889634f;
+  for (int i = 0; i < NS; ++i) A2[i] = ssm_log2(A2[i]);
   const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.Dskip ? p.Dskip[c] : 0.f;
 #pragma unroll
   for (int j = 0; j < SSM_STEP_B; ++j) {
@@ -530,8 +537,8 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 4) void ssm_bwd_local_ke
   const float* Arow = p.f.A + static_cast<long long>(c) * p.f.N;
 #pragma unroll
   for (int i = 0; i < NP / 2; ++i) {
-    A2[i].x = 2 * i < p.f.N ? Arow[2 * i] * 1.4426950408889634f : 0.f;
-    A2[i].y = 2 * i + 1 < p.f.N ? Arow[2 * i + 1] * 1.4426950408889634f : 0.f;
+    A2[i].x = 2 * i < p.f.N ? ssm_log2(Arow[2 * i]) : 0.f;
+    A2[i].y = 2 * i + 1 < p.f.N ? ssm_log2(Arow[2 * i + 1]) : 0.f;
     h[i] = g[i] = make_float2(0.f, 0.f);
     P[i] = make_float2(1.f, 1.f);
   }
@@ -608,7 +615,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p
   const int n = static_cast<int>(gid % per / p.f.D), c = static_cast<int>(gid % p.f.D);
   const bool on = n < p.f.N, back = blockIdx.y;
   const long long e = static_cast<long long>(c) * p.f.N + n, eb = static_cast<long long>(b) * p.f.D * p.f.N + e;
-  const float A2 = on ? p.f.A[e] * 1.4426950408889634f : 0.f;
+  const float A2 = on ? ssm_log2(p.f.A[e]) : 0.f;
   const int S = p.f.nseg;
   const long long first = back ? S - 1 : 0, step = back ? -1 : 1;
   float* vs = (back ? p.seg_g : p.f.seg_h) + (static_cast<long long>(b) * S + first) * per + gid % per;
@@ -775,8 +782,8 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
       for (int e = 0; e < 2; ++e) {
         const int n = q * NH + 2 * i;
         const float* Arow = p.f.A + static_cast<long long>(c + e) * N;
-        A[e][i].x = live && n < N ? Arow[n] : 0.f;
-        A[e][i].y = live && n + 1 < N ? Arow[n + 1] : 0.f;
+        A[e][i].x = live && n < N ? ssm_finite(Arow[n]) : 0.f;
+        A[e][i].y = live && n + 1 < N ? ssm_finite(Arow[n + 1]) : 0.f;
       }
     const float fbias = p.f.dt_bias ? p.f.dt_bias[cf] : 0.f, skip = p.f.Dskip ? p.f.Dskip[cf] : 0.f;
     chain_wait();

@@ -351,6 +351,31 @@ def test_scan_of_growing_states_that_are_still_zero(kta):
     assert torch.isfinite(S).all()
 
 
+@pytest.mark.parametrize("dtype,B,L,D,N,lens", [
+    (torch.float32, 1, 5, 8, 4, None), (torch.bfloat16, 2, 45, 40, 16, [45, 0]), (torch.float32, 1, 700, 16, 12, [333]),
+    (torch.bfloat16, 1, 33, 8, 32, None), (torch.bfloat16, 3, 1, 8, 8, None)])
+def test_scan_states_that_forget_at_once(kta, dtype, B, L, D, N, lens):
+    """A = -inf is A = -1e30 to the last bit: rows that pad a tile (d = 0) or lie behind a sequence leave the
+    state alone."""
+    r = np.random.default_rng(L)
+    x, kw, _ = scan_case(r, dtype, B, L, D, N, 1, True, True, True, True, lens)
+    do, dS = gpu(r.standard_normal((B, L, D)), dtype), gpu(r.standard_normal((B, D, N)))
+    some = torch.from_numpy(r.random((D, N)) < 0.5).cuda()
+    outs = []
+    for a in (-1e30, float("-inf")):
+        x["A"] = torch.where(some, a, x["A"])
+        y, S = kta.ssm_scan_fwd(**x, **kw, return_state=True)
+        g = kta.ssm_scan_bwd(**x, dout=do, dS_out=dS, **kw)
+        outs.append([y, S] + [t for t in g.values() if t is not None])
+        if L == 1:
+            one = {n: t if n == "A" else t[:, 0].contiguous() for n, t in x.items()}
+            state = kw["S0"].clone()
+            outs[-1] += [kta.ssm_scan_step(**one, state=state, D=kw["D"], z=kw["z"][:, 0].contiguous(),
+                                           dt_bias=kw["dt_bias"]), state]
+    assert all(torch.isfinite(t).all() for t in outs[0])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 @pytest.mark.parametrize("scale", [1e-30, -1e-20, 2.0 ** -126])
 def test_scan_of_small_states_that_grow(kta, scale):
     """A > 0: growth over one segment that overflows alone, while the state that it acts on stays finite; cut
