@@ -241,6 +241,7 @@ __global__ __launch_bounds__(SC_BWD_X* SC_BWD_Y, SC_BWD_BLOCKS) void short_conv_
           const uint64_t sg = f32x2_pack(rcp_approx(q.x), rcp_approx(q.y));
           const uint64_t cg = ffma2(sg, f32x2_pack(-1.f, -1.f), f32x2_pack(1.f, 1.f));
           g = fmul2(g, fmul2(sg, ffma2(a, cg, f32x2_pack(1.f, 1.f))));
+          if (!mine && s >= len) g = 0;       // no row: 0 times the slope of what is not finite is no 0
         }
         dp[K - 1][i] = g;
         if (mine) {

@@ -177,6 +177,29 @@ def test_short_conv_backward_of_runs_that_fill_the_card(kta):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("K", [2, 3, 4])
+def test_short_conv_backward_of_rows_behind_the_end(kta, dtype, K):
+    """Rows behind a sequence add nothing to its gradients, whatever their windows hold: the state of a slot
+    without rows, or a last row whose sum overflows behind the end alone."""
+    r = np.random.default_rng(K)
+    x, w, b, s, n, _ = conv_case(r, dtype, 2, 12, 16, K, True, True, [0, 12])
+    do, dS = gpu(r.standard_normal((2, 12, 16)), dtype), gpu(r.standard_normal((2, K - 1, 16)), dtype)
+    want = [kta.short_conv_bwd(x, w, do, b, S0=s, lens=n, dS_out=end) for end in (None, dS)]
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        s[0] = bad
+        for end, ok in zip((None, dS), want):
+            got = kta.short_conv_bwd(x, w, do, b, S0=s, lens=n, dS_out=end)
+            assert all(torch.equal(a, c) for a, c in zip(got, ok))
+            assert torch.equal(got[3][0], torch.zeros_like(dS[0]) if end is None else dS[0])
+    # the last row's own sum is 1e38 (the slope is 1 there), that of the row behind it infinite
+    x, w = torch.zeros(1, 9, 8, device="cuda", dtype=dtype), torch.zeros(8, K, device="cuda")
+    x[0, 8], w[:, K - 1], w[:, K - 2] = 2e38, 0.5, 2.0
+    do = torch.ones_like(x)
+    dx = kta.short_conv_bwd(x, w, do)[0]
+    assert (dx[0, 8] == 0.5).all() and torch.isfinite(dx).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [2, 3, 4])
 def test_short_conv_rollout_is_the_whole_sequence(kta, dtype, K):
     r = np.random.default_rng(K)
     x, w, b, s, _, _ = conv_case(r, dtype, 3, 11, 24, K, True, True, None)
