@@ -430,6 +430,15 @@ def test_rope_refuses_numbers_out_of_range(kta):
             kta.rope_fwd(q, freqs=f, **{"dims": 32, **kw})
 
 
+def test_sizes_past_their_c_types_are_value_errors(kta):
+    x = torch.empty(1, 1 << 31, 8, device="cuda", dtype=torch.bfloat16)     # 2^31 tokens
+    with pytest.raises(ValueError):
+        kta.short_conv_fwd(x, torch.zeros(8, 4, device="cuda"))
+    b = x.view(-1)[:1 << 31].view(1, 1 << 31, 1, 1)
+    with pytest.raises(ValueError):
+        kta.ssm_scan_fwd(x, x, torch.zeros(8, 1, device="cuda"), b, b)
+
+
 @pytest.mark.parametrize("dtype,N", [(torch.bfloat16, 16), (torch.bfloat16, 8), (torch.float32, 16)])
 def test_scan_rows_of_b_and_c_at_any_address(kta, dtype, N):
     """B and C, and the buffers of their gradients, may begin at any element."""
