@@ -577,8 +577,10 @@ _ROPE = struct.Struct("@7if P i q P")
 _CONV = struct.Struct("@6i 5P")
 _SSM = struct.Struct("@6i 10P")
 _GRADS = struct.Struct("@11P")
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream   # (device index) -> cudaStream_t
+# torch's own short ways to the current device and to a device's current cudaStream_t; a torch without them (one
+# built without CUDA has neither) takes the public ones, and imports.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _want(t, name, dtype, shape, dev):

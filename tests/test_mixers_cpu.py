@@ -264,3 +264,17 @@ def test_outputs_over_lengths_positions_or_frequencies_are_refused(kta):
                dict(x2=at(2), o2=at(3), H2=2, ld2=2, pos=at(3, 64)), dict(x2=at(2), o2=at(3), H2=2, ld2=2, freqs=at(3, 64)),
                dict(o=at(0), pos=at(0, 64))):
         assert rope_call(kta, **kw) == INVALID, kw
+
+
+def test_import_without_torchs_private_cuda_names(kta):
+    """A torch built without CUDA has no _cuda_* functions: the host-side checks are there all the same."""
+    import pathlib
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "from hybrid_linear_temporal_kta_b200 import kta\n"
+            "assert kta.version() > 0 and kta.rope_freqs(8, device='cpu')[0].numel() == 4\n")
+    root = pathlib.Path(kta.__file__).parents[1]
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
