@@ -343,6 +343,21 @@ def test_scan_long_segments_agree_with_pieces(kta):
     check("S in pieces", state, want["S_out"])
 
 
+def test_scan_step_sizes_to_their_stated_error(kta):
+    """With A = 0 and u = B = 1 the state after one token is d = log(1 + e^dt) itself. Relative error, in units of
+    2^-24: |x| for the rounded argument of e^-|x| and 0.23 |x| for log2(e) in fp32; 4 for the exponential, 0.5 for
+    the fit, 3 for its evaluation and 0.5 for the last sum."""
+    x = torch.linspace(-80, 20, 100_000, dtype=torch.float64).float().cuda()[None, None]
+    one = torch.ones(1, 1, 1, 1, device="cuda")
+    _, S = kta.ssm_scan_fwd(torch.ones_like(x), x, torch.zeros(x.shape[2], 1, device="cuda"), one, one, return_state=True)
+    step = kta.ssm_scan_step(torch.ones_like(x[0]), x[0], torch.zeros(x.shape[2], 1, device="cuda"), one[0], one[0],
+                             torch.zeros(1, x.shape[2], 1, device="cuda"))
+    want = np.logaddexp(0.0, host(x)[0, 0])
+    lim = want * (1.25 * np.abs(host(x)[0, 0]) + 8) * 2.0 ** -24
+    assert (np.abs(host(S)[0, :, 0] - want) <= lim).all()
+    assert (np.abs(host(step)[0] - want) <= lim).all()
+
+
 def test_scan_extreme_steps(kta):
     """Step sizes that under- and overflow: the state is kept exactly, or forgotten at once."""
     L, D, N = 40, 8, 16
