@@ -666,3 +666,54 @@ def test_offsets_past_32_bits(kta):
     f, _ = kta.rope_freqs(64)
     last = kta.rope_fwd(q[:, -3:].contiguous(), freqs=f, dims=64, pos0=131077)
     assert torch.equal(kta.rope_fwd(q, freqs=f, dims=64, out=q)[:, -3:], last)
+
+
+def zeros_but_the_last_rows(g, B, L, D, n):
+    x = torch.zeros(B, L, D, device="cuda", dtype=torch.bfloat16)
+    x[:, -n:] = torch.randn(B, n, D, device="cuda", generator=g).to(torch.bfloat16)
+    return x
+
+
+def test_backward_offsets_past_32_bits(kta):
+    """More than 2^31 elements a tensor, zeros but for the last rows: their gradients and the parameters' are
+    those of a call on the last rows alone."""
+    B, L, D, N, n = 2, 65537, 16392, 4, 8
+    g = torch.Generator("cuda").manual_seed(5)
+    x = zeros_but_the_last_rows(g, B, L, D, n)
+    tail = x[:, -n:].contiguous()
+    r = np.random.default_rng(5)
+    w, b = gpu(r.standard_normal((D, 4))), gpu(r.standard_normal(D))
+    dx, dw, db, _ = kta.short_conv_bwd(x, w, x, b)
+    want = mixers.short_conv(host(tail), host(w), host(b), dout=host(tail), bounds=True)
+    for name, t in (("dx", dx[:, -n:]), ("dw", dw), ("dbias", db)):
+        check(name, t, want[name])
+    del dx
+    A, Bm = gpu(-np.exp(r.uniform(-1, 1, (D, N)))), gpu(r.standard_normal((B, L, 1, N)), torch.bfloat16)
+    kw = {"D": gpu(r.standard_normal(D)), "dt_bias": gpu(r.standard_normal(D))}
+    got = kta.ssm_scan_bwd(x, x, A, Bm, Bm, x, **kw)
+    Bt = Bm[:, -n:].contiguous()
+    want = scan_oracle({"u": tail, "dt": tail, "A": A, "Bm": Bt, "Cm": Bt}, kw, None, dout=host(tail))
+    for name, t in got.items():
+        if t is not None:
+            check(name, t[:, -n:] if name in ("du", "ddt", "dB", "dC") else t, want[name])
+
+
+def test_segments_of_a_scan_with_offsets_past_32_bits(kta):
+    """2^28 tokens of 8 channels, cut into segments. Between the first rows and the last d = 0, so the state
+    stays as it is, and the ends come out as if they were neighbours."""
+    L, D, N, n = (1 << 28) + 77, 8, 4, 16
+    r = np.random.default_rng(6)
+    ends = {k: gpu(r.standard_normal((1, 2 * n) + tail), torch.bfloat16)
+            for k, tail in (("u", (D,)), ("dt", (D,)), ("Bm", (1, N)), ("Cm", (1, N)))}
+
+    def stretch(t, fill):
+        x = torch.full((1, L) + t.shape[2:], fill, device="cuda", dtype=t.dtype)
+        x[:, :n], x[:, -n:] = t[:, :n], t[:, n:]
+        return x
+
+    A = gpu(-np.exp(r.uniform(-3, -1, (D, N))))
+    x = {k: stretch(t, -200.0 if k == "dt" else 1.0) for k, t in ends.items()}
+    y, S = kta.ssm_scan_fwd(**x, A=A, return_state=True)
+    want = scan_oracle({**ends, "A": A}, {}, None)
+    check("y", torch.cat([y[:, :n], y[:, -n:]], 1), want["y"])
+    check("S_out", S, want["S_out"])

@@ -278,3 +278,39 @@ def test_import_without_torchs_private_cuda_names(kta):
             "assert kta.version() > 0 and kta.rope_freqs(8, device='cpu')[0].numel() == 4\n")
     root = pathlib.Path(kta.__file__).parents[1]
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+
+
+STRUCTS = [("Rope", "kta_rope", "_ROPE"), ("ShortConv", "kta_short_conv", "_CONV"), ("Ssm", "kta_ssm", "_SSM"),
+           ("SsmGrads", "kta_ssm_grads", "_GRADS")]
+
+
+def test_struct_layouts_are_the_headers(kta, tmp_path):
+    """Sizes and offsets of the ctypes structures as a C compiler lays them out."""
+    import pathlib
+    import subprocess
+    lines = [f'printf("%zu", sizeof({c}));' + "".join(f' printf(" %zu", offsetof({c}, {f[0]}));' for f in getattr(kta, py)._fields_)
+             + ' printf("\\n");' for py, c, _ in STRUCTS]
+    src = "#include <stddef.h>\n#include <stdio.h>\n#include \"kta.h\"\nint main(void) {\n" + "\n".join(lines) + "\nreturn 0; }\n"
+    (tmp_path / "a.c").write_text(src)
+    inc = pathlib.Path(kta.__file__).parents[1] / "include"
+    subprocess.run(["gcc", f"-I{inc}", "-o", tmp_path / "a", tmp_path / "a.c"], check=True)
+    out = subprocess.run([tmp_path / "a"], check=True, capture_output=True, text=True).stdout.splitlines()
+    for (py, _, _), line in zip(STRUCTS, out, strict=True):
+        t = getattr(kta, py)
+        assert [int(v) for v in line.split()] == [ctypes.sizeof(t)] + [getattr(t, f[0]).offset for f in t._fields_], py
+
+
+def test_packed_structs_are_the_ctypes_structures(kta):
+    """What calls pack natively is, byte for byte, the structure that the library is declared to take."""
+    for py, _, packed in STRUCTS:
+        t, flat, fields = getattr(kta, py), [], []
+        for i, (name, ty) in enumerate(t._fields_):
+            if name == "dims":
+                v = [101, 102, 103, 104]
+                fields.append((ctypes.c_int * 4)(*v))
+                flat += v
+            else:
+                v = 0.25 + i if ty is ctypes.c_float else (7 + i << 33) + i if ctypes.sizeof(ty) == 8 else (1 << 20) + i
+                fields.append(v)
+                flat.append(v)
+        assert getattr(kta, packed).pack(*flat) == bytes(t(*fields)), py
