@@ -8,6 +8,8 @@
 #pragma once
 #include <float.h>
 
+#include <type_traits>
+
 #include "mixer_common.cuh"
 
 namespace kta {
@@ -76,9 +78,13 @@ __device__ __forceinline__ void ssm_store_states(float* row, int q, int N, const
   }
 }
 
-// log2(e) A, kept finite: an infinite A then forgets (or grows) at every step d > 0 and leaves the state alone
-// where d = 0, as in the rows that pad a tile.
-__device__ __forceinline__ float ssm_finite(float x) { return fabsf(x) > FLT_MAX ? copysignf(FLT_MAX, x) : x; }
+// A = -inf as the lowest finite value (a NaN stays one): every step d > 0 forgets, and where d = 0, as in the
+// rows that pad a tile, the state stays.
+__device__ __forceinline__ float ssm_finite(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-FLT_MAX));
+  return y;
+}
 __device__ __forceinline__ float ssm_log2(float A) { return ssm_finite(A * 1.4426950408889634f); }
 
 // Starts the copies of TT rows of B (and of C, if C) to their raw tile.
@@ -325,13 +331,34 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 3 : 4) void ssm_fwd_kernel(c
 // states that enter them. Loads of SSM_CARRY_UNROLL segments are in flight at once.
 constexpr int SSM_CARRY_UNROLL = 8;
 
-// 2^x h + v. Where a segment's growth alone overflows (A > 0) it is applied in two halves: 2^x h is then formed
-// whenever h and it are normal numbers, and a state still at zero stays there.
+// 2^x h + v; a state still at zero stays there. GROW: where a segment's growth alone overflows (A > 0), 2^126 of
+// it goes to h first (exactly), so that 2^x h is formed whenever h and it are normal numbers.
+template <bool GROW>
 __device__ __forceinline__ float ssm_carry(float x, float h, float v) {
-  if (h == 0.f) return v;
-  if (x < 128.f) return fmaf(ex2_approx(x), h, v);
-  const float half = ex2_approx(0.5f * x);
-  return fmaf(half, half * h, v);
+  const bool up = GROW && x >= 128.f;
+  const float e = ex2_approx(up ? x - 126.f : x);
+  return h == 0.f ? v : fmaf(e, up ? h * 0x1p126f : h, v);
+}
+
+// Up to SSM_CARRY_UNROLL segments in a row, `vstep` elements apart: their end states from zero (v, loaded from vs)
+// become the states that enter them; d: their sums of d.
+__device__ __forceinline__ void ssm_carry_batch(float* vs, long long vstep, const float (&v)[SSM_CARRY_UNROLL],
+                                                const float (&d)[SSM_CARRY_UNROLL], float A2, int left, float& h) {
+  bool grow = false;                                     // uncommon, and one test for all
+#pragma unroll
+  for (int i = 0; i < SSM_CARRY_UNROLL; ++i) grow |= d[i] * A2 >= 128.f;
+  auto walk = [&](auto up) {
+#pragma unroll
+    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
+      if (i < left) {
+        vs[i * vstep] = h;
+        h = ssm_carry<decltype(up)::value>(d[i] * A2, h, v[i]);
+      }
+  };
+  if (grow)
+    walk(std::true_type());
+  else
+    walk(std::false_type());
 }
 
 __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, int NP) {
@@ -350,16 +377,13 @@ __global__ __launch_bounds__(256) void ssm_fwd_carry_kernel(const SsmParams p, i
     float v[SSM_CARRY_UNROLL], d[SSM_CARRY_UNROLL];
 #pragma unroll
     for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
-      if (s0 + i < p.nseg - 1) {
+      if (s0 + i < p.nseg - 1) {                         // (what follows the last segment is not wanted)
         v[i] = hs[(s0 + i) * per];
         d[i] = ds[static_cast<long long>(s0 + i) * p.D];
+      } else {
+        v[i] = d[i] = 0.f;
       }
-#pragma unroll
-    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
-      if (s0 + i < p.nseg) {
-        hs[(s0 + i) * per] = h;
-        if (s0 + i < p.nseg - 1) h = ssm_carry(d[i] * A2, h, v[i]);
-      }
+    ssm_carry_batch(hs + s0 * per, per, v, d, A2, p.nseg - s0, h);
   }
 }
 
@@ -629,13 +653,10 @@ __global__ __launch_bounds__(256) void ssm_bwd_carry_kernel(const SsmBwdParams p
       if (s0 + i < S) {
         v[i] = vs[step * (s0 + i) * per];
         d[i] = ds[step * (s0 + i) * p.f.D];
+      } else {
+        v[i] = d[i] = 0.f;
       }
-#pragma unroll
-    for (int i = 0; i < SSM_CARRY_UNROLL; ++i)
-      if (s0 + i < S) {
-        vs[step * (s0 + i) * per] = h;
-        h = ssm_carry(d[i] * A2, h, v[i]);
-      }
+    ssm_carry_batch(vs + step * s0 * per, step * per, v, d, A2, S - s0, h);
   }
   if (back && on && p.dS0) p.dS0[eb] = h;
 }
@@ -782,8 +803,8 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
       for (int e = 0; e < 2; ++e) {
         const int n = q * NH + 2 * i;
         const float* Arow = p.f.A + static_cast<long long>(c + e) * N;
-        A[e][i].x = live && n < N ? ssm_finite(Arow[n]) : 0.f;
-        A[e][i].y = live && n + 1 < N ? ssm_finite(Arow[n + 1]) : 0.f;
+        A[e][i].x = live && n < N ? Arow[n] : 0.f;
+        A[e][i].y = live && n + 1 < N ? Arow[n + 1] : 0.f;
       }
     const float fbias = p.f.dt_bias ? p.f.dt_bias[cf] : 0.f, skip = p.f.Dskip ? p.f.Dskip[cf] : 0.f;
     chain_wait();
@@ -791,6 +812,10 @@ __global__ __launch_bounds__(SSM_THREADS, NP > 16 ? 2 : 3) void ssm_bwd_main_ker
     load_pairs(sg, g);
     piece_wait<0>();
     __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e)                        // (here the loads of A are in without a wait of their own)
+#pragma unroll
+      for (int i = 0; i < H2; ++i) A[e][i] = make_float2(ssm_finite(A[e][i].x), ssm_finite(A[e][i].y));
     {
       const int cc = lane % CH;                        // a lane's items have one channel
       const bool con = wc + cc < k.cw;
