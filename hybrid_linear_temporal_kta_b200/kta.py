@@ -738,10 +738,10 @@ def _conv_args(x, w, bias, silu, S0, lens, step=False):
     if w.dim() != 2:
         raise ValueError("w must be [D, K]")
     K = w.shape[1]
-    at = (at, _want(w, "w", torch.float32, (D, K), dev), _want(bias, "bias", torch.float32, (D,), dev),
-          _want(S0, "S0", ty, (B, K - 1, D), dev), _want(lens, "lens", torch.int32, (B,), dev))
     try:
-        c = _CONV.pack(B, 1 if step else x.shape[1], D, K, dt, bool(silu), *at)
+        c = _CONV.pack(B, 1 if step else x.shape[1], D, K, dt, bool(silu), at,
+                       _want(w, "w", torch.float32, (D, K), dev), _want(bias, "bias", torch.float32, (D,), dev),
+                       _want(S0, "S0", ty, (B, K - 1, D), dev), _want(lens, "lens", torch.int32, (B,), dev))
     except struct.error as e:
         raise ValueError(f"x is too large: {e}") from None
     return c, ty, dev, (B, K - 1, D)
@@ -826,12 +826,12 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, step=False):
     B, C, N, G = shape[0], shape[-1], A.shape[1], Bm.shape[-2]
     bc = shape[:-1] + (G, N)
     states = (B, C, N)
-    at = (at, _want(dt, "dt", ty, shape, dev), _want(A, "A", f32, (C, N), dev), _want(Bm, "Bm", ty, bc, dev),
-          _want(Cm, "Cm", ty, bc, dev), _want(D, "D", f32, (C,), dev), _want(z, "z", ty, shape, dev),
-          _want(dt_bias, "dt_bias", f32, (C,), dev), _want(S0, "S0", f32, states, dev),
-          _want(lens, "lens", torch.int32, (B,), dev))
     try:
-        c = _SSM.pack(B, 1 if step else shape[1], C, N, G, code, *at)
+        c = _SSM.pack(B, 1 if step else shape[1], C, N, G, code, at, _want(dt, "dt", ty, shape, dev),
+                      _want(A, "A", f32, (C, N), dev), _want(Bm, "Bm", ty, bc, dev),
+                      _want(Cm, "Cm", ty, bc, dev), _want(D, "D", f32, (C,), dev),
+                      _want(z, "z", ty, shape, dev), _want(dt_bias, "dt_bias", f32, (C,), dev),
+                      _want(S0, "S0", f32, states, dev), _want(lens, "lens", torch.int32, (B,), dev))
     except struct.error as e:
         raise ValueError(f"u is too large: {e}") from None
     return c, ty, dev, states
