@@ -214,9 +214,9 @@ int conv_run(const kta_short_conv* c) {
 }
 
 // Backward: runs are stretched towards a whole number of turns of the card where that shortens the path of its
-// busiest SM. A turn of k blocks there takes (run + K - 1) (2 + 4 k) units: a row costs a warp half as
-// much again as its share of the SM's issue. (Fits 120 measured plans to 2 %.) us with runs of 64 / of the
-// stretched length, turns of the card as the stretched blocks fill it:
+// busiest SM. There a row of k blocks takes 2 + 4 k units: one for each warp, and two whatever their number.
+// (Fits 120 measured plans to 2 %; one choice in 60 was the slower by more than that: 4 %.) us with runs of
+// 64 / of the stretched length, and the turns of the card that the stretched blocks fill:
 //   stretched: 2 x 3,600 x 4,096  67.0 / 58.3 (0.97), 2 x 12,000 x 2,048  97.1 / 91.0 (2.00),
 //     8 x 1,759 x 7,936  197.5 / 187.7 (4.19);
 //   kept: 8 x 768 x 5,120  66.6 / 80.8 (0.54), 24 x 512 x 4,096  97.2 / 103.3 (1.30),

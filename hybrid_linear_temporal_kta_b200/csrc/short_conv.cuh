@@ -7,8 +7,9 @@
 // A thread owns 4 channels and walks a run of tokens with the last K - 1 rows in registers, so every row
 // is read once per run plus the K - 1 rows before it, which its neighbour has brought into L2. Weights and
 // sums are fp32. Forward: memory-bound, 2 x 65,536 x 2,048 bf16 (1.07 GB moved) in 192 us, a copy of as
-// many bytes 171 us; 8 channels to a thread need twice the registers: 260 us. Backward: bound by
-// its 36 instructions per element: 2 x 8,191 x 2,048 bf16 (201 MB) in 64 us, bytes alone 31.
+// many bytes 171 us; 8 channels to a thread need twice the registers: 260 us. Backward: 2 x 8,191 x 2,048 bf16
+// (201 MB) in 64 us, where the bytes alone take 31 and the issue of its 36 instructions per element 33: the two
+// follow each other instead of overlapping.
 #pragma once
 #include "mixer_common.cuh"
 

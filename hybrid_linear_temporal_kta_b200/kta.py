@@ -749,11 +749,11 @@ def _conv_args(x, w, bias, silu, S0, lens, step=False):
 
 def short_conv_fwd(x, w, bias=None, *, silu: bool = True, S0=None, lens=None,
                    return_state: bool = False, out=None, stream=None):
-    """Causal convolution of x [B, L, D] (bf16 or fp32) with one filter per channel, w [D, K] fp32
-    (K = 2, 3, 4; the last tap is the token's own), bias [D] fp32, then silu. S0 [B, K-1, D]: the rows
-    before the first (zeros without). lens [B] int32: rows of each sequence; o is left alone past them
-    (fresh buffers are zero there) and the end state is taken there. Returns o (and the last K - 1
-    rows)."""
+    """Causal convolution of x [B, L, D] (bf16 or fp32; contiguous, as every tensor here) with one filter per
+    channel, w [D, K] fp32 (K = 2, 3, 4; the last tap is the token's own), bias [D] fp32, then silu. S0 [B,
+    K-1, D]: the rows before the first (zeros without). lens [B] int32: rows of each sequence; o is left
+    alone past them (fresh buffers are zero there) and the end state is taken there. Returns o (and the last
+    K - 1 rows)."""
     c, ty, dev, rows = _conv_args(x, w, bias, silu, S0, lens)
     _want(out, "out", ty, x.shape, dev)
 
@@ -839,10 +839,10 @@ def _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens, step=False):
 
 def ssm_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, S0=None, lens=None,
                  return_state: bool = False, out=None, stream=None):
-    """Selective state-space scan of u [B, L, D] (bf16 or fp32): h_t = exp(d_t A) h_{t-1} + d_t u_t B_t
-    with d = softplus(dt + dt_bias), y = (C . h + D u) silu(z). dt, z like u; A [D, N] fp32; Bm, Cm
-    [B, L, G, N] like u, group g for channels g D/G ..; D, dt_bias [D] fp32; S0 [B, D, N] fp32. lens
-    [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
+    """Selective state-space scan of u [B, L, D] (bf16 or fp32; every tensor contiguous): h_t = exp(d_t A)
+    h_{t-1} + d_t u_t B_t with d = softplus(dt + dt_bias), y = (C . h + D u) silu(z). dt, z like u; A [D, N]
+    fp32; Bm, Cm [B, L, G, N] like u, group g for channels g D/G ..; D, dt_bias [D] fp32; S0 [B, D, N] fp32.
+    lens [B] int32: rows of each sequence; y is left alone past them (fresh buffers are zero there) and the
     end state is taken there. Returns y (and the end state)."""
     c, ty, dev, states = _ssm_args(u, dt, A, Bm, Cm, D, z, dt_bias, S0, lens)
     _want(out, "out", ty, u.shape, dev)

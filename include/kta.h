@@ -432,7 +432,8 @@ kta_status kta_rope_freqs(int dims, double base, int scaling, double factor, dou
  * paper-read's GLA paragraph names as the branch's basis, has one; the pages do not show it):
  *     pre_t = bias + sum_{j<K} w_j x_{t-K+1+j},   o_t = silu(pre_t) (silu = 1) or pre_t.
  *  - x, o: [B][L][D] (dtype); w: [D][K] fp32; bias: [D] fp32 or NULL. K in {2, 3, 4}; D % 8 == 0;
- *    B*L < 2^31 - 2^16; every pointer 16-byte aligned.
+ *    B*L < 2^31 - 2^16; every pointer 16-byte aligned. Rows are dense (D is their stride): columns of a
+ *    wider projection, or some heads of a tensor, are copied out first.
  *  - S0: [B][K-1][D] (dtype), the K - 1 rows before the first (oldest first), or NULL = zeros.
  *    S_out: the last K - 1 rows of [S0; x], or NULL. S_out = S0 updates the state in place; with
  *    L = 1 this is the step of a rollout.
@@ -441,8 +442,9 @@ kta_status kta_rope_freqs(int dims, double base, int scaling, double factor, dou
  *  - No output may overlap another tensor (but S_out = S0).
  * kta_short_conv_bwd: dx [B][L][D] (rows past a sequence's end are left), dw [D][K], dbias [D]
  * or NULL (fp32), dS0 [B][K-1][D] or NULL; dS_out: gradient of S_out or NULL. Sums run in a fixed
- * order: the same call gives the same bits. ws: kta_short_conv_bwd_workspace(c) bytes of device
- * memory, 16-byte aligned, for this call alone until it has run (0 from the query = bad arguments).
+ * order: the same call gives the same bits. ws: kta_short_conv_bwd_workspace(c) bytes (asked with the
+ * same device current: it depends on its SMs) of device memory, 16-byte aligned, for this call alone
+ * until it has run (0 from the query = bad arguments).
  */
 typedef struct {
   int B, L, D, K;
@@ -472,7 +474,8 @@ kta_status kta_short_conv_bwd(const kta_short_conv* c, const void* dout, const v
  *    the states themselves within fp32's normal range, the backward pass exp(A sum d) over 32 tokens too);
  *    D_skip, dt_bias: [D] fp32 or NULL (= 0);
  *    z NULL = no gate. 1 <= N <= 32; G divides D; (D / G) % 8 == 0; B*L < 2^31 - 2^16; every pointer
- *    16-byte aligned, but Bm, Cm and their gradients by their element alone.
+ *    16-byte aligned, but Bm, Cm and their gradients by their element alone. Rows are dense. A may be -inf
+ *    (every step forgets).
  *  - S0, S_out: [B][D][N] fp32, the state before the first and after the last token; NULL = zero / not
  *    wanted. States and sums are fp32; y is rounded once.
  *  - lens: as in kta_short_conv.
