@@ -176,6 +176,27 @@ def test_short_conv_backward_of_runs_that_fill_the_card(kta):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_parameter_gradients_over_many_rows_and_few_channels(kta, dtype):
+    """Hundreds of partial sums for a few columns: dw and dbias of the convolution, dA, dD and ddt_bias of the scan."""
+    r = np.random.default_rng(21)
+    x, w, b, _, n, seen = conv_case(r, dtype, 2, 4500, 8, 4, True, False, [4500, 4001])
+    do = gpu(r.standard_normal(x.shape), dtype)
+    do[1, 4001:] = float("nan")
+    got = kta.short_conv_bwd(x, w, do, b, lens=n)
+    want = mixers.short_conv(np.nan_to_num(host(x)), host(w), host(b), lens=seen, dout=np.nan_to_num(host(do)), bounds=True)
+    for name, g in zip(("dx", "dw", "dbias"), got):
+        check(name, g, want[name])
+    x, kw, seen = scan_case(r, dtype, 2, 4500, 8, 4, 1, True, True, True, False, [4001, 4500])
+    do = gpu(r.standard_normal(x["u"].shape), dtype)
+    do[0, 4001:] = float("nan")
+    got = kta.ssm_scan_bwd(**x, dout=do, **kw)
+    want = scan_oracle(x, kw, seen, dout=np.nan_to_num(host(do)))
+    for name, g in got.items():
+        if g is not None:
+            check(name, g, want[name])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("K", [2, 3, 4])
 def test_short_conv_backward_of_rows_behind_the_end(kta, dtype, K):
     """Rows behind a sequence add nothing to its gradients, whatever their windows hold: the state of a slot
